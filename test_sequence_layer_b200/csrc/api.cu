@@ -70,7 +70,7 @@ mesa_status launch_forward(const ForwardArgs& a, cudaStream_t st) {
 // ---- kernel timing records ----
 const char* const kKindNames[kKindCount] = {"simt_scan", "simt_cg", "decode_step", "tc_scan", "tc_cg",
                                              "preprocess", "bwd_adjoint", "bwd_rscan", "bwd_grad", "bwd_reduce",
-                                             "shard", "bwd_rhs"};
+                                             "shard", "bwd_rhs", "lru", "lru_bwd", "swa", "swa_bwd", "swa_step"};
 struct TimingRec {
     int kind;
     cudaEvent_t start, stop;

@@ -56,7 +56,8 @@ unsigned* error_word_ptr();
 // Kernel kinds for the optional timing records (mesa_timing_enable).
 enum KernelKind : int {
     kKindSimtScan = 0, kKindSimtCg, kKindStep, kKindTcScan, kKindTcCg, kKindPre,
-    kKindBwdAdj, kKindBwdRscan, kKindBwdGrad, kKindBwdReduce, kKindShard, kKindBwdRhs, kKindCount
+    kKindBwdAdj, kKindBwdRscan, kKindBwdGrad, kKindBwdReduce, kKindShard, kKindBwdRhs,
+    kKindLru, kKindLruBwd, kKindSwa, kKindSwaBwd, kKindSwaStep, kKindCount
 };
 
 // Brackets one launch with CUDA events on `st` while timing is enabled.

@@ -1,0 +1,456 @@
+// swa_step.cu -- one decoded token of sliding-window attention over a rolling
+// cache (mesa_swa_step), and the cache after a prompt (mesa_swa_cache_fill).
+//
+// The cache's bytes bound the step, so its slots are split over the warps of a
+// cluster of CTAs (1 to 16), each warp with its own running maximum, sum and
+// output rows; the parts are joined once at the end, first in a CTA's shared
+// memory and then through distributed shared memory, so a step is one launch
+// without a workspace.
+//
+// The new token's rows are read from the arguments, not from the cache: their
+// slot is written by one CTA while others run, and nobody reads it.
+#include <cooperative_groups.h>
+#include <math.h>
+
+#include "mesa_common.cuh"
+#include "mesa_internal.h"
+#include "mixers_internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace mesa {
+namespace {
+
+constexpr int kMaxSplits = 16;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ int slot_of(int p, int window, int sinks) {
+    return p < sinks ? p : sinks + (p - sinks) % window;
+}
+
+// ---- parts of one CTA, joined over the cluster ----
+// rows x D outputs with maximum m (in log2 units) and sum l per row
+template <int ROWS, int D> struct Part {
+    float o[ROWS][D];
+    float m[ROWS], l[ROWS];
+};
+
+template <typename T> __device__ __forceinline__ T to_out(float v);
+template <> __device__ __forceinline__ float to_out<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// out rows [0, rows) of the joined parts; every CTA of the cluster calls it
+template <typename T, int ROWS, int D>
+__device__ __forceinline__ void join(Part<ROWS, D>& part, int splits, int rank, int rows, T* out) {
+    cg::cluster_group cl = cg::this_cluster();
+    if (splits > 1) cl.sync(); else __syncthreads();
+    for (int i = rank * blockDim.x + threadIdx.x; i < rows * D; i += splits * blockDim.x) {
+        const int r = i / D, c = i % D;
+        float m = -INFINITY, l = 0.f, o = 0.f;
+        for (int s = 0; s < splits; ++s) {
+            const Part<ROWS, D>* q = splits > 1 ? cl.map_shared_rank(&part, s) : &part;
+            m = fmaxf(m, q->m[r]);
+        }
+        for (int s = 0; s < splits; ++s) {
+            const Part<ROWS, D>* q = splits > 1 ? cl.map_shared_rank(&part, s) : &part;
+            const float w = exp2f(q->m[r] - m);            // a part without slots: exp2(-inf) = 0
+            l = fmaf(q->l[r], w, l);
+            o = fmaf(q->o[r][c], w, o);
+        }
+        out[i] = to_out<T>(o / l);
+    }
+    if (splits > 1) cl.sync();                             // no CTA leaves while its part may be read
+}
+
+struct Row {                                               // what a CTA needs to know of its sequence
+    int own, n;                                            // the token's slot, slots in use
+};
+
+// ---- fp32 on the CUDA cores: any type, d in {16, 32, 64, 128} ----
+constexpr int kSimtRows = 8, kSimtThreads = 128;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kSimtThreads) swa_step_simt_kernel(SwaStepArgs p, int splits) {
+    constexpr int kParts = kSimtThreads / D;               // threads that share a channel
+    __shared__ Part<kSimtRows, D> part;
+    __shared__ float sq[kSimtRows][D], sw[kSimtRows][kSimtThreads], keep[kSimtRows];
+    __shared__ float so[kParts][kSimtRows][D];
+    const int G = p.Hq / p.Hkv, hgroups = (G + kSimtRows - 1) / kSimtRows;
+    const int rank = blockIdx.x % splits, b = blockIdx.z, hk = blockIdx.y / hgroups;
+    const int h0 = (blockIdx.y % hgroups) * kSimtRows, rows = min(kSimtRows, G - h0);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    T* out = static_cast<T*>(p.out) + ((size_t)b * p.Hq + hk * G + h0) * D;
+    const int pos = p.pos[b];
+    if (pos < 0) {                                         // the same for the whole cluster
+        for (int i = rank * kSimtThreads + tid; i < rows * D; i += splits * kSimtThreads) out[i] = to_out<T>(0.f);
+        return;
+    }
+    const int cap = p.sinks + p.window, own = slot_of(pos, p.window, p.sinks);
+    const int n = pos < cap - 1 ? pos + 1 : cap;
+    const T* kin = static_cast<const T*>(p.k) + ((size_t)b * p.Hkv + hk) * D;
+    const T* vin = static_cast<const T*>(p.v) + ((size_t)b * p.Hkv + hk) * D;
+    T* kc = static_cast<T*>(p.kc) + ((size_t)b * p.Hkv + hk) * cap * D;
+    T* vc = static_cast<T*>(p.vc) + ((size_t)b * p.Hkv + hk) * cap * D;
+    if (rank == 0 && h0 == 0)
+        for (int c = tid; c < D; c += kSimtThreads) {
+            kc[(size_t)own * D + c] = kin[c];
+            vc[(size_t)own * D + c] = vin[c];
+        }
+    for (int i = tid; i < kSimtRows * D; i += kSimtThreads) {
+        const int r = i / D, c = i % D;
+        sq[r][c] = r < rows ? ld_in(static_cast<const T*>(p.q), ((size_t)b * p.Hq + hk * G + h0 + r) * D + c) *
+                                  (p.scale * kLog2e) : 0.f;
+    }
+    float o[kSimtRows];
+#pragma unroll
+    for (int r = 0; r < kSimtRows; ++r) o[r] = 0.f;
+    if (tid < kSimtRows) part.m[tid] = -INFINITY, part.l[tid] = 0.f;
+    __syncthreads();
+    for (int s0 = rank * kSimtThreads; s0 < n; s0 += splits * kSimtThreads) {
+        float s[kSimtRows];
+#pragma unroll
+        for (int r = 0; r < kSimtRows; ++r) s[r] = 0.f;
+        const int slot = s0 + tid;
+        if (slot < n) {
+            const T* kr = slot == own ? kin : kc + (size_t)slot * D;
+#pragma unroll 4
+            for (int c = 0; c < D; ++c) {
+                const float kv = ld_in(kr, c);
+#pragma unroll
+                for (int r = 0; r < kSimtRows; ++r) s[r] = fmaf(sq[r][c], kv, s[r]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kSimtRows; ++r) sw[r][tid] = slot < n ? s[r] : -INFINITY;
+        __syncthreads();
+        for (int r = warp; r < kSimtRows; r += kSimtThreads / 32) {
+            float m0 = part.m[r], m = m0, l = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = fmaxf(m, sw[r][lane + 32 * i]);
+#pragma unroll
+            for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float e = exp2f(sw[r][lane + 32 * i] - m);     // slot s0 is in use: m is finite
+                sw[r][lane + 32 * i] = e;
+                l += e;
+            }
+#pragma unroll
+            for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(~0u, l, x);
+            __syncwarp();
+            if (lane == 0) {
+                keep[r] = exp2f(m0 - m);
+                part.m[r] = m;
+                part.l[r] = part.l[r] * keep[r] + l;
+            }
+        }
+        __syncthreads();
+        const int c = tid % D, first = tid / D, last = min(kSimtThreads, n - s0);
+#pragma unroll
+        for (int r = 0; r < kSimtRows; ++r) o[r] *= keep[r];
+        for (int i = first; i < last; i += kParts) {
+            const float vv = ld_in(s0 + i == own ? vin : vc + (size_t)(s0 + i) * D, c);
+#pragma unroll
+            for (int r = 0; r < kSimtRows; ++r) o[r] = fmaf(sw[r][i], vv, o[r]);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < kSimtRows; ++r) so[tid / D][r][tid % D] = o[r];
+    __syncthreads();
+    for (int i = tid; i < kSimtRows * D; i += kSimtThreads) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kParts; ++w) v += so[w][i / D][i % D];
+        part.o[i / D][i % D] = v;
+    }
+    join<T, kSimtRows, D>(part, splits, rank, rows, out);
+}
+
+// ---- bf16, d in {64, 128}: warp-level matrix instructions ----
+// Per 16 slots a warp forms S = Q K^T (rows: up to 8 or 16 heads, columns:
+// slots) and O += P V with m16n8k16. The contraction over d and the order of
+// d in the output may be permuted, so every fragment is a plain 16-byte load
+// of a cache row: for S a lane takes pieces c, c + 4, ... of rows g and g + 8
+// (g = lane / 4, c = lane % 4), for O piece g of rows 2c, 2c + 1, 2c + 8,
+// 2c + 9, whose halves are paired with byte permutes. No shared memory and no
+// barrier in the loop; the next 16 slots of K and V are in flight meanwhile.
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint4 ld16(const __nv_bfloat16* p) {
+    return *reinterpret_cast<const uint4*>(p);
+}
+
+constexpr int kMmaWarps = 4, kMmaThreads = kMmaWarps * 32;
+
+// ROWS = 8 or 16 heads of the group per CTA
+template <int ROWS, int D>
+__global__ void __launch_bounds__(kMmaThreads) swa_step_mma_kernel(SwaStepArgs p, int splits) {
+    constexpr int kPieces = D / 32;                        // 16-byte pieces of a K row per lane
+    constexpr int kSets = D / 64;                          // 64-wide runs of d in a V row
+    using bf = __nv_bfloat16;
+    extern __shared__ float4 smem4[];
+    Part<ROWS, D>* parts = reinterpret_cast<Part<ROWS, D>*>(smem4);      // one per warp
+    const int G = p.Hq / p.Hkv, hgroups = (G + ROWS - 1) / ROWS;
+    const int rank = blockIdx.x % splits, b = blockIdx.z, hk = blockIdx.y / hgroups;
+    const int h0 = (blockIdx.y % hgroups) * ROWS, rows = min(ROWS, G - h0);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    bf* out = static_cast<bf*>(p.out) + ((size_t)b * p.Hq + hk * G + h0) * D;
+    const int pos = p.pos[b];
+    if (pos < 0) {
+        for (int i = rank * kMmaThreads + tid; i < rows * D; i += splits * kMmaThreads) out[i] = to_out<bf>(0.f);
+        return;
+    }
+    const int cap = p.sinks + p.window, own = slot_of(pos, p.window, p.sinks);
+    const int n = pos < cap - 1 ? pos + 1 : cap;
+    const bf* kin = static_cast<const bf*>(p.k) + ((size_t)b * p.Hkv + hk) * D;
+    const bf* vin = static_cast<const bf*>(p.v) + ((size_t)b * p.Hkv + hk) * D;
+    bf* kc = static_cast<bf*>(p.kc) + ((size_t)b * p.Hkv + hk) * cap * D;
+    bf* vc = static_cast<bf*>(p.vc) + ((size_t)b * p.Hkv + hk) * cap * D;
+    if (rank == 0 && h0 == 0 && tid < D / 8) {
+        reinterpret_cast<uint4*>(kc + (size_t)own * D)[tid] = ld16(kin + tid * 8);
+        reinterpret_cast<uint4*>(vc + (size_t)own * D)[tid] = ld16(vin + tid * 8);
+    }
+    // rows the token's own slot or no token holds come from the arguments (the latter at weight 0)
+    auto krow = [&](int slot) { return slot == own || slot >= n ? kin : kc + (size_t)slot * D; };
+    auto vrow = [&](int slot) { return slot == own || slot >= n ? vin : vc + (size_t)slot * D; };
+    uint4 kr[2][kPieces], vr[4][kSets];
+    auto fetch_k = [&](int s0) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const bf* r = krow(s0 + 8 * t + g);
+#pragma unroll
+            for (int u = 0; u < kPieces; ++u) kr[t][u] = ld16(r + (c + 4 * u) * 8);
+        }
+    };
+    auto fetch_v = [&](int s0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bf* r = vrow(s0 + 2 * c + (i & 1) + 8 * (i >> 1));
+#pragma unroll
+            for (int u = 0; u < kSets; ++u) vr[i][u] = ld16(r + (g + 8 * u) * 8);
+        }
+    };
+    const int stride = splits * kMmaWarps * 16;
+    int s0 = (rank * kMmaWarps + warp) * 16;
+    if (s0 < n) {
+        fetch_k(s0);
+        fetch_v(s0);
+    }
+    uint4 q0[kPieces], q1[kPieces];
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        const bf* qr = static_cast<const bf*>(p.q) + ((size_t)b * p.Hq + hk * G + h0) * D + (c + 4 * u) * 8;
+        q0[u] = g < rows ? ld16(qr + (size_t)g * D) : z;
+        q1[u] = ROWS > 8 && g + 8 < rows ? ld16(qr + (size_t)(g + 8) * D) : z;
+    }
+    const float sc = p.scale * kLog2e;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[kSets * 8][4];
+#pragma unroll
+    for (int i = 0; i < kSets * 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    for (; s0 < n; s0 += stride) {
+        float s[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+#pragma unroll
+            for (int u = 0; u < kPieces; ++u) {
+                mma_bf16(s[t], q0[u].x, q1[u].x, q0[u].y, q1[u].y, kr[t][u].x, kr[t][u].y);
+                mma_bf16(s[t], q0[u].z, q1[u].z, q0[u].w, q1[u].w, kr[t][u].z, kr[t][u].w);
+            }
+        }
+        const bool more = s0 + stride < n;
+        if (more) fetch_k(s0 + stride);
+        uint32_t pa[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < (ROWS > 8 ? 2 : 1); ++r) {
+            float v[4], mx = m[r];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int slot = s0 + 8 * (i >> 1) + 2 * c + (i & 1);
+                v[i] = slot < n ? s[i >> 1][2 * r + (i & 1)] * sc : -INFINITY;
+                mx = fmaxf(mx, v[i]);
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+            const float keep = exp2f(m[r] - mx);                     // slot s0 is in use: mx is finite
+            if (__any_sync(~0u, mx > m[r])) {
+#pragma unroll
+                for (int i = 0; i < kSets * 8; ++i) o[i][2 * r] *= keep, o[i][2 * r + 1] *= keep;
+                l[r] *= keep;
+            }
+            m[r] = mx;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = exp2f(v[i] - mx);
+                l[r] += v[i];
+            }
+            pa[r] = pack_bf16(v[0], v[1]);
+            pa[2 + r] = pack_bf16(v[2], v[3]);
+        }
+#pragma unroll
+        for (int u = 0; u < kSets; ++u) {
+            const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vr[0][u]);
+            const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vr[1][u]);
+            const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vr[2][u]);
+            const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vr[3][u]);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                mma_bf16(o[8 * u + 2 * w], pa[0], pa[1], pa[2], pa[3], __byte_perm(v0[w], v1[w], 0x5410),
+                         __byte_perm(v2[w], v3[w], 0x5410));
+                mma_bf16(o[8 * u + 2 * w + 1], pa[0], pa[1], pa[2], pa[3], __byte_perm(v0[w], v1[w], 0x7632),
+                         __byte_perm(v2[w], v3[w], 0x7632));
+            }
+        }
+        if (more) fetch_v(s0 + stride);
+    }
+    // column n of tile j holds d = 64 u + 8 n + j
+#pragma unroll
+    for (int r = 0; r < (ROWS > 8 ? 2 : 1); ++r) {
+        l[r] += __shfl_xor_sync(~0u, l[r], 1);
+        l[r] += __shfl_xor_sync(~0u, l[r], 2);
+        Part<ROWS, D>& w = parts[warp];
+        const int row = g + 8 * r;
+        if (c == 0) w.m[row] = m[r], w.l[row] = l[r];
+#pragma unroll
+        for (int u = 0; u < kSets; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int j = 0; j < 8; j += 4)
+                    *reinterpret_cast<float4*>(&w.o[row][64 * u + 8 * (2 * c + e) + j]) =
+                        make_float4(o[8 * u + j][2 * r + e], o[8 * u + j + 1][2 * r + e],
+                                    o[8 * u + j + 2][2 * r + e], o[8 * u + j + 3][2 * r + e]);
+    }
+    __syncthreads();
+    // the warps' parts into the first one's place: each element by one thread
+    for (int i = tid; i < rows * D; i += kMmaThreads) {
+        const int r = i / D, d = i % D;
+        float mm = parts[0].m[r], v = 0.f;
+#pragma unroll
+        for (int w = 1; w < kMmaWarps; ++w) mm = fmaxf(mm, parts[w].m[r]);
+        const float ref = mm == -INFINITY ? 0.f : mm;        // a CTA without slots
+#pragma unroll
+        for (int w = 0; w < kMmaWarps; ++w) v = fmaf(parts[w].o[r][d], exp2f(parts[w].m[r] - ref), v);
+        parts[0].o[r][d] = v;
+    }
+    __syncthreads();
+    if (tid < rows) {
+        float mm = parts[0].m[tid], v = 0.f;
+#pragma unroll
+        for (int w = 1; w < kMmaWarps; ++w) mm = fmaxf(mm, parts[w].m[tid]);
+        const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+        for (int w = 0; w < kMmaWarps; ++w) v = fmaf(parts[w].l[tid], exp2f(parts[w].m[tid] - ref), v);
+        parts[0].m[tid] = mm;
+        parts[0].l[tid] = v;
+    }
+    join<bf, ROWS, D>(parts[0], splits, rank, rows, out);
+}
+
+// ---- rolling cache of a prompt ----
+__global__ void swa_cache_fill_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v, uint4* kc, uint4* vc,
+                                      const int32_t* __restrict__ lens, int Hkv, int S, int units, int window,
+                                      int sinks, int start) {
+    const int bh = blockIdx.y, b = bh / Hkv, cap = sinks + window;
+    const int len = lens ? min(max(lens[b], 0), S) : S;
+    const int end = start + len;
+    const size_t total = (size_t)cap * units;
+    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (size_t)gridDim.x * blockDim.x) {
+        const int slot = (int)(i / units), u = (int)(i % units);
+        int p = slot;                                     // the last position before end that lives in the slot
+        if (slot >= sinks) {
+            const int last = end - 1 - slot;              // counted from the slot's first position
+            if (last < 0) continue;
+            p = slot + last / window * window;
+        }
+        if (p < start || p >= end) continue;
+        const size_t src = ((size_t)bh * S + (p - start)) * units + u;
+        kc[(size_t)bh * total + i] = k[src];
+        vc[(size_t)bh * total + i] = v[src];
+    }
+}
+
+template <typename F>
+cudaError_t launch_step(F* kernel, const SwaStepArgs& a, int rows_per_cta, int slots_per_round, int threads,
+                        int smem, cudaStream_t st) {
+    const int G = a.Hq / a.Hkv, hgroups = (G + rows_per_cta - 1) / rows_per_cta;
+    const long long blocks = (long long)a.B * a.Hkv * hgroups;
+    // CTAs per head and sequence: doubled while the grid is below three CTAs
+    // per SM and every CTA's warps still get a run of slots
+    int splits = 1;
+    while (splits < kMaxSplits && blocks * splits < 3 * 148 &&
+           (long long)2 * splits * slots_per_round <= (long long)a.sinks + a.window)
+        splits *= 2;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && splits > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(splits, a.Hkv * hgroups, a.B);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = splits;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a, splits);
+}
+
+template <int ROWS, int D>
+cudaError_t step_mma(const SwaStepArgs& a, cudaStream_t st) {
+    return launch_step(swa_step_mma_kernel<ROWS, D>, a, ROWS, kMmaWarps * 16, kMmaThreads,
+                       (int)sizeof(Part<ROWS, D>) * kMmaWarps, st);
+}
+
+template <typename T>
+cudaError_t step_simt(const SwaStepArgs& a, cudaStream_t st) {
+    switch (a.d) {
+        case 16: return launch_step(swa_step_simt_kernel<T, 16>, a, kSimtRows, kSimtThreads, kSimtThreads, 0, st);
+        case 32: return launch_step(swa_step_simt_kernel<T, 32>, a, kSimtRows, kSimtThreads, kSimtThreads, 0, st);
+        case 64: return launch_step(swa_step_simt_kernel<T, 64>, a, kSimtRows, kSimtThreads, kSimtThreads, 0, st);
+        default: return launch_step(swa_step_simt_kernel<T, 128>, a, kSimtRows, kSimtThreads, kSimtThreads, 0, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t swa_step(const SwaStepArgs& a, cudaStream_t st) {
+    LaunchTimer lt(kKindSwaStep, st);
+    if (a.dtype == MESA_F32) return step_simt<float>(a, st);
+    const bool wide = a.Hq / a.Hkv > 8;
+    if (a.d == 128) return wide ? step_mma<16, 128>(a, st) : step_mma<8, 128>(a, st);
+    if (a.d == 64) return wide ? step_mma<16, 64>(a, st) : step_mma<8, 64>(a, st);
+    return step_simt<__nv_bfloat16>(a, st);
+}
+
+cudaError_t swa_cache_fill(const void* k, const void* v, void* kc, void* vc, const int32_t* lens, int B, int Hkv,
+                           int S, int d, int window, int sinks, int start, mesa_dtype dtype, cudaStream_t st) {
+    LaunchTimer lt(kKindSwaStep, st);
+    const int units = d * (dtype == MESA_F32 ? 4 : 2) / 16;
+    const size_t total = (size_t)(sinks + window) * units;
+    const unsigned gx = (unsigned)((total + 255) / 256 < 4096 ? (total + 255) / 256 : 4096);
+    swa_cache_fill_kernel<<<dim3(gx, B * Hkv), 256, 0, st>>>(static_cast<const uint4*>(k), static_cast<const uint4*>(v),
+                                                             static_cast<uint4*>(kc), static_cast<uint4*>(vc), lens, Hkv,
+                                                             S, units, window, sinks, start);
+    return cudaGetLastError();
+}
+
+}  // namespace mesa

@@ -82,6 +82,26 @@ def _load():
     lib.mesa_backward_workspace_size.restype = Z
     lib.mesa_backward.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, P, P, P, P, P, P, P, P, Z, P]
     lib.mesa_backward.restype = I
+    lib.mesa_lru_saved_size.argtypes = [I, I, I]
+    lib.mesa_lru_saved_size.restype = Z
+    lib.mesa_lru_forward.argtypes = [P, P, P, P, I, I, I, I, P, P, P, P, P]
+    lib.mesa_lru_forward.restype = I
+    lib.mesa_lru_backward_workspace_size.argtypes = [I, I, I, I, I]
+    lib.mesa_lru_backward_workspace_size.restype = Z
+    lib.mesa_lru_backward.argtypes = [P, P, P, P, I, I, I, I, P, P, P, P, P, P, P, P, P, P, Z, P]
+    lib.mesa_lru_backward.restype = I
+    lib.mesa_lru_step.argtypes = [P, P, P, P, I, I, I, P, P, P, P]
+    lib.mesa_lru_step.restype = I
+    lib.mesa_swa_forward.argtypes = [P, P, P, I, I, I, I, I, I, I, I, F, I, P, P, P]
+    lib.mesa_swa_forward.restype = I
+    lib.mesa_swa_backward_workspace_size.argtypes = [I, I, I, I, I, I, I, I]
+    lib.mesa_swa_backward_workspace_size.restype = Z
+    lib.mesa_swa_backward.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, I, P, P, P, P, Z, P]
+    lib.mesa_swa_backward.restype = I
+    lib.mesa_swa_step.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, F, I, P, P]
+    lib.mesa_swa_step.restype = I
+    lib.mesa_swa_cache_fill.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, P]
+    lib.mesa_swa_cache_fill.restype = I
     _lib = lib
     return lib
 
@@ -378,7 +398,7 @@ def timing_enable(on: bool = True):
 def timing_read() -> dict:
     """{kernel kind: (launches, total device ms)} since the last read (synchronises)."""
     lib = _load()
-    n = 16
+    n = 32
     names = (ctypes.c_char_p * n)()
     launches = (ctypes.c_int * n)()
     ms = (ctypes.c_double * n)()
@@ -408,3 +428,249 @@ def forward_noalloc(q, k, v, gamma, beta, lam, *, chunk=64, cg_steps=15, tol=0.0
                                   _ptr(H_in), _ptr(G_in), _ptr(H_out), _ptr(G_out), _stream(stream, q.device))
     _check(rc, "mesa_forward_noalloc")
     return out
+
+
+# ---- the other mixers of a hybrid stack (include/mesa_mixers.h) ----
+
+def _arg(name, t, shape, dtype, device):
+    """A CUDA tensor the library may take by its pointer: shape, type, device, contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _first(name, t, dims):
+    """The argument that fixes type, sizes and device of a call."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    return _arg(name, t, t.shape, t.dtype, t.device)
+
+
+class _On:
+    """Runs a call on the tensors' device; what it allocates belongs to its stream."""
+
+    def __init__(self, device, stream):
+        self.device = torch.cuda.device(device)
+        self.stream = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+def _workspace(given, need, device):
+    if given is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    if not given.is_cuda or given.device != device or not given.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
+    return given
+
+
+def _lru_inputs(x, gate_a, gate_x, lam, dims):
+    _first("x", x, dims)
+    if x.shape[0] < 1 or x.shape[-1] < 1:
+        raise ValueError(f"x needs at least one sequence and one channel, got {tuple(x.shape)}")
+    _arg("gate_a", gate_a, x.shape, x.dtype, x.device)
+    _arg("gate_x", gate_x, x.shape, x.dtype, x.device)
+    _arg("lam", lam, x.shape[-1:], torch.float32, x.device)
+
+
+def lru_forward(x, gate_a, gate_x, lam, *, h0=None, y=None, return_state=False, return_saved=False, stream=None):
+    """Gated linear recurrence over a sequence (mesa_lru_forward):
+    h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(gate_x_t) x_t with
+    log a_t = -8 softplus(lam) sigmoid(gate_a_t).
+
+    x, gate_a, gate_x: [B,T,D] float32 or bfloat16; lam: [D] float32;
+    h0: [B,D] float32 or None (zero). Returns y [B,T,D] in x's type, plus the
+    final state [B,D] float32 if return_state, plus the states lru_backward
+    takes ([B, ceil(T/64), D] float32) if return_saved.
+    """
+    lib = _load()
+    _lru_inputs(x, gate_a, gate_x, lam, 3)
+    (B, T, D), dev = x.shape, x.device
+    if h0 is not None:
+        _arg("h0", h0, (B, D), torch.float32, dev)
+    if y is not None:
+        _arg("y", y, x.shape, x.dtype, dev)
+    with _On(dev, stream):
+        y = torch.empty_like(x) if y is None else y
+        h_T = torch.empty((B, D), dtype=torch.float32, device=dev) if return_state else None
+        saved = torch.empty((B, -(-T // 64), D), dtype=torch.float32, device=dev) if return_saved else None
+        _check(lib.mesa_lru_forward(_ptr(x), _ptr(gate_a), _ptr(gate_x), _ptr(lam), B, T, D, _dtype_code(x), _ptr(h0),
+                                    _ptr(y), _ptr(h_T), _ptr(saved), _stream(stream, dev)), "mesa_lru_forward")
+    res = (y,) + ((h_T,) if return_state else ()) + ((saved,) if return_saved else ())
+    return res[0] if len(res) == 1 else res
+
+
+def lru_backward(x, gate_a, gate_x, lam, dy, *, h0=None, saved=None, dh_T=None, workspace=None, stream=None):
+    """Gradients of lru_forward (mesa_lru_backward) given dy = dL/dy [B,T,D]
+    and dh_T = dL/dh_T [B,D] float32 (None: zero). `saved` is what lru_forward
+    returned for these inputs; without it the states are recomputed from h0.
+    Returns (dx, dgate_a, dgate_x, dlam, dh0): the first three in x's type,
+    dlam [D] and dh0 [B,D] float32."""
+    lib = _load()
+    _lru_inputs(x, gate_a, gate_x, lam, 3)
+    (B, T, D), dev, code = x.shape, x.device, _dtype_code(x)
+    _arg("dy", dy, x.shape, x.dtype, dev)
+    if h0 is not None:
+        _arg("h0", h0, (B, D), torch.float32, dev)
+    if saved is not None:
+        _arg("saved", saved, (B, -(-T // 64), D), torch.float32, dev)
+    if dh_T is not None:
+        _arg("dh_T", dh_T, (B, D), torch.float32, dev)
+    with _On(dev, stream):
+        dx, dga, dgx = (torch.empty_like(x) for _ in range(3))
+        dlam = torch.empty(D, dtype=torch.float32, device=dev)
+        dh0 = torch.empty((B, D), dtype=torch.float32, device=dev)
+        need = int(lib.mesa_lru_backward_workspace_size(B, T, D, code, saved is not None))
+        workspace = _workspace(workspace, need, dev)
+        _check(lib.mesa_lru_backward(_ptr(x), _ptr(gate_a), _ptr(gate_x), _ptr(lam), B, T, D, code, _ptr(h0),
+                                     _ptr(saved), _ptr(dy), _ptr(dh_T), _ptr(dx), _ptr(dga), _ptr(dgx), _ptr(dlam),
+                                     _ptr(dh0), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                     _stream(stream, dev)), "mesa_lru_backward")
+    return dx, dga, dgx, dlam, dh0
+
+
+def lru_step(x, gate_a, gate_x, lam, h, *, h_out=None, y=None, stream=None):
+    """One decoded token of the recurrence (mesa_lru_step): x, gate_a, gate_x
+    [B,D]; the state h [B,D] float32 is updated in place, or left as it is and
+    the new one written to h_out. Returns y [B,D] in x's type."""
+    lib = _load()
+    _lru_inputs(x, gate_a, gate_x, lam, 2)
+    (B, D), dev = x.shape, x.device
+    _arg("h", h, (B, D), torch.float32, dev)
+    if h_out is not None:
+        _arg("h_out", h_out, (B, D), torch.float32, dev)
+    if y is not None:
+        _arg("y", y, x.shape, x.dtype, dev)
+    with _On(dev, stream):
+        y = torch.empty_like(x) if y is None else y
+        _check(lib.mesa_lru_step(_ptr(x), _ptr(gate_a), _ptr(gate_x), _ptr(lam), B, D, _dtype_code(x), _ptr(h),
+                                 _ptr(h if h_out is None else h_out), _ptr(y), _stream(stream, dev)), "mesa_lru_step")
+    return y
+
+
+def _swa_inputs(q, k, v, dims):
+    """Checks q [B,Hq,(T,)d] against k, v [B,Hkv,(S,)d]."""
+    _first("q", q, dims)
+    if not isinstance(k, torch.Tensor) or k.dim() != dims:
+        raise ValueError(f"k must be a tensor of {dims} dimensions")
+    if k.shape[0] != q.shape[0] or k.shape[-1] != q.shape[-1]:
+        raise ValueError(f"k {tuple(k.shape)} does not go with q {tuple(q.shape)}")
+    _arg("k", k, k.shape, q.dtype, q.device)
+    _arg("v", v, k.shape, q.dtype, q.device)
+
+
+def _size(name, v):
+    """A size the C ABI takes as a 32-bit integer; its range is checked there."""
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} = {v} does not fit 32 bits")
+    return v
+
+
+def _scale(scale, d):
+    return float(d) ** -0.5 if scale is None else float(scale)
+
+
+def swa_forward(q, k, v, *, window, sinks=0, scale=None, out=None, return_lse=False, stream=None):
+    """Causal sliding-window attention with sinks (mesa_swa_forward).
+
+    q: [B,Hq,T,d]; k, v: [B,Hkv,S,d] (float32 or bfloat16, one type), Hq a
+    multiple of Hkv, S >= T: the queries are the last T positions. Position p
+    sees key j if j <= p and (p - j < window or j < sinks); d in {16,32,64,128},
+    sinks <= 128. scale defaults to 1/sqrt(d). Returns out [B,Hq,T,d] in q's
+    type, plus lse [B,Hq,T] float32 if return_lse.
+    """
+    lib = _load()
+    _swa_inputs(q, k, v, 4)
+    (B, Hq, T, d), (_, Hkv, S, _), dev = q.shape, k.shape, q.device
+    if out is not None:
+        _arg("out", out, q.shape, q.dtype, dev)
+    with _On(dev, stream):
+        out = torch.empty_like(q) if out is None else out
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev) if return_lse else None
+        _check(lib.mesa_swa_forward(_ptr(q), _ptr(k), _ptr(v), B, Hq, Hkv, T, S, d, _size("window", window), _size("sinks", sinks),
+                                    _scale(scale, d), _dtype_code(q), _ptr(out), _ptr(lse), _stream(stream, dev)),
+               "mesa_swa_forward")
+    return (out, lse) if return_lse else out
+
+
+def swa_backward(q, k, v, out, lse, dout, *, window, sinks=0, scale=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dv), in the inputs' type, of swa_forward for the
+    same arguments, from its out and lse and dout = dL/dout (mesa_swa_backward)."""
+    lib = _load()
+    _swa_inputs(q, k, v, 4)
+    (B, Hq, T, d), (_, Hkv, S, _), dev, code = q.shape, k.shape, q.device, _dtype_code(q)
+    _arg("out", out, q.shape, q.dtype, dev)
+    _arg("lse", lse, (B, Hq, T), torch.float32, dev)
+    _arg("dout", dout, q.shape, q.dtype, dev)
+    with _On(dev, stream):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        need = int(lib.mesa_swa_backward_workspace_size(B, Hq, Hkv, T, S, d, _size("sinks", sinks), code))
+        workspace = _workspace(workspace, need, dev)
+        _check(lib.mesa_swa_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), B, Hq, Hkv, T, S, d,
+                                     _size("window", window), _size("sinks", sinks), _scale(scale, d), code, _ptr(dq), _ptr(dk), _ptr(dv),
+                                     _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                     _stream(stream, dev)), "mesa_swa_backward")
+    return dq, dk, dv
+
+
+def _caches(k_cache, v_cache, B, Hkv, slots, d, dtype, device):
+    _arg("k_cache", k_cache, (B, Hkv, slots, d), dtype, device)
+    _arg("v_cache", v_cache, (B, Hkv, slots, d), dtype, device)
+
+
+def swa_step(q, k, v, k_cache, v_cache, pos, *, window, sinks=0, scale=None, out=None, stream=None):
+    """One decoded token over rolling caches (mesa_swa_step): q [B,Hq,d],
+    k, v [B,Hkv,d], k_cache, v_cache [B,Hkv,sinks+window,d] updated in place,
+    pos [B] int32 on the device: the token's position, negative for an idle
+    row (its caches untouched, its output zero). Returns out [B,Hq,d]."""
+    lib = _load()
+    _swa_inputs(q, k, v, 3)
+    (B, Hq, d), Hkv, dev = q.shape, k.shape[1], q.device
+    _caches(k_cache, v_cache, B, Hkv, _size("sinks", sinks) + _size("window", window), d, q.dtype, dev)
+    _arg("pos", pos, (B,), torch.int32, dev)
+    if out is not None:
+        _arg("out", out, q.shape, q.dtype, dev)
+    with _On(dev, stream):
+        out = torch.empty_like(q) if out is None else out
+        _check(lib.mesa_swa_step(_ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(pos), B, Hq, Hkv, d,
+                                 _size("window", window), _size("sinks", sinks), _scale(scale, d), _dtype_code(q), _ptr(out),
+                                 _stream(stream, dev)), "mesa_swa_step")
+    return out
+
+
+def swa_cache_fill(k, v, k_cache, v_cache, *, window, sinks=0, start=0, lens=None, stream=None):
+    """Puts the tokens k, v [B,Hkv,S,d] at positions start, start + 1, ...
+    into rolling caches (mesa_swa_cache_fill), as S swa_step calls would.
+    lens: int32 [B] on the device, the tokens of each sequence (None: S)."""
+    lib = _load()
+    _first("k", k, 4)
+    (B, Hkv, S, d), dev = k.shape, k.device
+    _arg("v", v, k.shape, k.dtype, dev)
+    _caches(k_cache, v_cache, B, Hkv, _size("sinks", sinks) + _size("window", window), d, k.dtype, dev)
+    if lens is not None:
+        _arg("lens", lens, (B,), torch.int32, dev)
+    with _On(dev, stream):
+        _check(lib.mesa_swa_cache_fill(_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(lens), B, Hkv, S, d,
+                                       _size("window", window), _size("sinks", sinks), _size("start", start), _dtype_code(k), _stream(stream, dev)),
+               "mesa_swa_cache_fill")

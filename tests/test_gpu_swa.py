@@ -1,0 +1,351 @@
+"""Sliding-window attention with sinks on the GPU against its definition in 64 bits."""
+import pytest
+import torch
+
+import mixers_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mesa():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from test_sequence_layer_b200 import build, mesa
+    build.build()
+    return mesa
+
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def inputs(B, Hq, Hkv, T, S, d, dtype, seed=0, gain=1.0):
+    g = torch.Generator().manual_seed(seed)
+
+    def one(*shape):
+        return torch.randn(shape, generator=g).cuda()
+    q, k, v, do = one(B, Hq, T, d), one(B, Hkv, S, d), one(B, Hkv, S, d), one(B, Hq, T, d)
+    return (q * gain).to(DT[dtype]), k.to(DT[dtype]), v.to(DT[dtype]), do.to(DT[dtype])
+
+
+# (B, Hq, Hkv, T, S, window, sinks)
+CASES = [
+    (1, 1, 1, 1, 1, 1, 0), (1, 2, 1, 1, 5, 3, 1), (2, 2, 2, 2, 2, 7, 1), (1, 1, 1, 5, 5, 1, 0), (1, 1, 1, 5, 5, 1, 2),
+    (1, 3, 1, 63, 63, 20, 4), (1, 2, 2, 64, 64, 64, 0), (1, 4, 2, 65, 65, 64, 1), (2, 2, 1, 127, 127, 33, 3),
+    (1, 2, 1, 128, 128, 128, 4), (1, 2, 1, 129, 129, 127, 4), (1, 4, 4, 200, 200, 500, 0), (1, 2, 1, 257, 257, 1, 4),
+    (1, 2, 1, 300, 300, 100, 64), (1, 2, 1, 300, 300, 50, 65), (1, 2, 1, 400, 400, 90, 128), (1, 1, 1, 260, 260, 2, 128),
+    (1, 2, 1, 1, 400, 100, 4), (2, 4, 2, 77, 333, 100, 5), (1, 2, 1, 130, 700, 129, 4), (1, 8, 1, 513, 513, 256, 4),
+    (1, 2, 2, 129, 1000, 300, 0), (1, 16, 2, 200, 330, 140, 33), (1, 2, 1, 1000, 1000, 250, 17),
+]
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+def test_forward_and_backward(mesa, case, dtype, d):
+    B, Hq, Hkv, T, S, window, sinks = case
+    q, k, v, do = inputs(B, Hq, Hkv, T, S, d, dtype, seed=T + S)
+    kw = dict(window=window, sinks=sinks)
+    out, lse = mesa.swa_forward(q, k, v, return_lse=True, **kw)
+    want = ref.swa(q, k, v, window, sinks, matrix=ref.matrix_path(q.dtype, d), dout=do)
+    ref.check(out, *want["out"], "out")
+    ref.check(lse, *want["lse"], "lse")
+    grads = mesa.swa_backward(q, k, v, out, lse, do, **kw)
+    for n, g in zip(("dq", "dk", "dv"), grads):
+        ref.check(g, *want[n], n)
+    assert torch.equal(out, mesa.swa_forward(q, k, v, **kw))
+    for a, b in zip(grads, mesa.swa_backward(q, k, v, out, lse, do, **kw)):
+        assert torch.equal(a, b)                                      # no order of atomics in it
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 32), ("bf16", 64), ("bf16", 128)])
+def test_scale_and_large_scores(mesa, dtype, d):
+    """A scale of the caller's, and scores far apart: the running maximum moves from tile to tile."""
+    q, k, v, do = inputs(1, 2, 1, 300, 420, d, dtype, seed=2, gain=6.0)
+    k *= torch.linspace(0.1, 3.0, 420, device="cuda").to(k)[:, None]
+    for scale in (0.05, 0.3):
+        out, lse = mesa.swa_forward(q, k, v, window=200, sinks=9, scale=scale, return_lse=True)
+        want = ref.swa(q, k, v, 200, 9, scale=scale, matrix=ref.matrix_path(q.dtype, d), dout=do)
+        ref.check(out, *want["out"], "out")
+        ref.check(lse, *want["lse"], "lse")
+        for n, g in zip(("dq", "dk", "dv"), mesa.swa_backward(q, k, v, out, lse, do, window=200, sinks=9, scale=scale)):
+            ref.check(g, *want[n], n)
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 16), ("bf16", 128)])
+def test_gradients_against_differences(mesa, dtype, d):
+    q, k, v, do = inputs(1, 4, 2, 90, 150, d, dtype, seed=3)
+    out, lse = mesa.swa_forward(q, k, v, window=40, sinks=3, return_lse=True)
+    grads = mesa.swa_backward(q, k, v, out, lse, do, window=40, sinks=3)
+    want = ref.swa(q, k, v, 40, 3, matrix=ref.matrix_path(q.dtype, d), dout=do)
+    args = [t.double() for t in (q, k, v)]
+    gen = torch.Generator().manual_seed(1)
+    for i, n in enumerate(("dq", "dk", "dv")):
+        dr = torch.randn(args[i].shape, generator=gen, dtype=torch.float64).cuda()
+        up, dn = list(args), list(args)
+        up[i], dn[i] = args[i] + 1e-5 * dr, args[i] - 1e-5 * dr
+        diff = sum(s * (ref.swa(*a, 40, 3)["out"][0] * do.double()).sum() for s, a in ((1, up), (-1, dn))) / 2e-5
+        val, bound = want[n]
+        slack = ((bound + ref.half_step(q.dtype) * (val.abs() + bound)) * dr.abs()).sum()
+        assert abs(float(diff - (grads[i].double() * dr).sum())) <= float(slack) + 1e-5 * float((val * dr).abs().sum())
+
+
+def test_no_queries(mesa):
+    q, k, v, do = inputs(1, 2, 1, 0, 50, 64, "bf16")
+    out, lse = mesa.swa_forward(q, k, v, window=10, return_lse=True)
+    assert out.shape == q.shape and lse.shape == (1, 2, 0)
+    dq, dk, dv = mesa.swa_backward(q, k, v, out, lse, do, window=10)
+    assert torch.count_nonzero(dk) == 0 and torch.count_nonzero(dv) == 0
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
+def test_rows_behind_a_sequence_do_not_matter(mesa, dtype, d):
+    """A right-padded batch: what the padding holds changes nothing before it, and
+    zero gradients there leave it out of the sums."""
+    T, n = 300, 211
+    q, k, v, do = inputs(2, 2, 1, T, T, d, dtype, seed=4)
+    do[1, :, n:] = 0
+    kw = dict(window=64, sinks=4)
+    out, lse = mesa.swa_forward(q, k, v, return_lse=True, **kw)
+    g = mesa.swa_backward(q, k, v, out, lse, do, **kw)
+    q2, k2, v2 = q.clone(), k.clone(), v.clone()
+    q2[1, :, n:], k2[1, :, n:], v2[1, :, n:] = 100.0, -50.0, 1000.0
+    out2, lse2 = mesa.swa_forward(q2, k2, v2, return_lse=True, **kw)
+    g2 = mesa.swa_backward(q2, k2, v2, out2, lse2, do, **kw)
+    assert torch.equal(out[1, :, :n], out2[1, :, :n]) and torch.equal(out[0], out2[0])
+    for a, b in zip(g, g2):
+        assert torch.equal(a[1, :, :n], b[1, :, :n]) and torch.count_nonzero(b[1, :, n:]) == 0
+
+
+def test_stream_and_graph(mesa):
+    a = inputs(1, 4, 2, 200, 260, 128, "bf16", seed=5)
+    b = inputs(1, 4, 2, 200, 260, 128, "bf16", seed=6)
+    q, k, v, do = (t.clone() for t in a)
+    kw = dict(window=100, sinks=4)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = mesa.swa_forward(q, k, v, stream=s, **kw)
+    s.synchronize()
+    assert torch.equal(out, mesa.swa_forward(q, k, v, **kw))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        oc, lc = mesa.swa_forward(q, k, v, return_lse=True, **kw)
+        gc = mesa.swa_backward(q, k, v, oc, lc, do, **kw)
+    for t, n in zip((q, k, v, do), b):
+        t.copy_(n)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    o, l = mesa.swa_forward(b[0], b[1], b[2], return_lse=True, **kw)
+    assert torch.equal(oc, o) and torch.equal(lc, l)
+    for x, y in zip(gc, mesa.swa_backward(b[0], b[1], b[2], o, l, b[3], **kw)):
+        assert torch.equal(x, y)
+
+
+def test_two_streams_at_once(mesa):
+    """Calls that overlap, each with its own workspace."""
+    sets = [inputs(2, 4, 2, 700, 700, 128, "bf16", seed=i) for i in (10, 11)]
+    kw = dict(window=200, sinks=4)
+    want = []
+    for q, k, v, do in sets:
+        o, l = mesa.swa_forward(q, k, v, return_lse=True, **kw)
+        want.append((o, l) + mesa.swa_backward(q, k, v, o, l, do, **kw))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [None, None]
+    for _ in range(3):
+        for i, (s, (q, k, v, do)) in enumerate(zip(streams, sets)):
+            o, l = mesa.swa_forward(q, k, v, return_lse=True, stream=s, **kw)
+            got[i] = (o, l) + mesa.swa_backward(q, k, v, o, l, do, stream=s, **kw)
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for a, b in zip(g, w):
+            assert torch.equal(a, b)
+
+
+def test_refusals(mesa):
+    q, k, v, do = inputs(1, 4, 2, 20, 30, 64, "bf16")
+    kw = dict(window=8, sinks=2)
+    out, lse = mesa.swa_forward(q, k, v, return_lse=True, **kw)
+    with pytest.raises(TypeError):
+        mesa.swa_forward(q.half(), k, v, **kw)
+    with pytest.raises(TypeError):
+        mesa.swa_forward(q, k.float(), v, **kw)
+    with pytest.raises(ValueError):
+        mesa.swa_forward(q, k, v[:, :, :5], **kw)
+    with pytest.raises(ValueError):
+        mesa.swa_forward(q.transpose(1, 2), k, v, **kw)
+    with pytest.raises(ValueError):
+        mesa.swa_forward(q, k, v, window=2 ** 32 + 1)
+    for bad, status in ((dict(window=0), 1), (dict(window=4, sinks=-1), 1), (dict(window=4, sinks=129), 2),
+                        (dict(window=4, scale=float("nan")), 1), (dict(window=4, scale=0.0), 1)):
+        with pytest.raises(mesa.MesaError) as e:
+            mesa.swa_forward(q, k, v, **bad)
+        assert e.value.status == status
+    with pytest.raises(mesa.MesaError) as e:
+        mesa.swa_forward(q[:, :3].contiguous(), k, v, **kw)           # 3 heads over 2
+    assert e.value.status == 1
+    with pytest.raises(mesa.MesaError) as e:
+        mesa.swa_forward(k, q[:, :2].contiguous(), q[:, :2].contiguous(), **kw)      # more queries than keys
+    assert e.value.status == 1
+    with pytest.raises(mesa.MesaError) as e:
+        mesa.swa_forward(q, k, v, out=q, **kw)
+    assert e.value.status == 1
+    with pytest.raises(mesa.MesaError) as e:
+        mesa.swa_backward(q, k, v, out, lse, do, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"), **kw)
+    assert e.value.status == 3
+
+
+# ---- decode ----
+
+def step_ref(q, kc, vc, pos, window, sinks, matrix):
+    """Rows of (out, bound) from caches that already hold the new token."""
+    B, Hq, d = q.shape
+    Hkv = kc.shape[1]
+    outs, bounds = [], []
+    for b in range(B):
+        p = int(pos[b])
+        seen = [j for j in range(min(sinks, p + 1))] + list(range(max(sinks, p - window + 1), p + 1))
+        at = [j if j < sinks else sinks + (j - sinks) % window for j in seen]
+        r = ref.swa(q[b:b + 1, :, None], kc[b:b + 1, :, at], vc[b:b + 1, :, at], len(at), 0, matrix=matrix)["out"]
+        outs.append(r[0][:, :, 0])
+        bounds.append(r[1][:, :, 0])
+    return torch.cat(outs), torch.cat(bounds)
+
+
+STEPS = [  # (B, Hq, Hkv, window, sinks)
+    (1, 1, 1, 1, 0), (2, 2, 1, 1, 3), (3, 4, 2, 7, 2), (2, 8, 8, 33, 1), (4, 8, 1, 64, 4), (2, 16, 1, 100, 0),
+    (2, 24, 1, 130, 5), (5, 12, 4, 257, 4), (1, 16, 2, 1500, 128), (1, 9, 1, 4000, 4),
+]
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", STEPS, ids=lambda c: "-".join(map(str, c)))
+def test_step(mesa, case, dtype, d):
+    B, Hq, Hkv, window, sinks = case
+    cap = window + sinks
+    g = torch.Generator().manual_seed(cap + d)
+    kc, vc = (torch.randn(B, Hkv, cap, d, generator=g).cuda().to(DT[dtype]) for _ in range(2))
+    for trial in range(4):
+        pos = [[0, cap - 1, cap, 3 * cap + 1, 2 ** 31 - 1], [1, sinks, cap - 2, 5 * cap, cap // 2],
+               [-1, cap // 3, 2 * cap, 0, 1], [sinks + 1, cap, -1, -7, cap + 3]][trial]
+        pos = torch.tensor([max(p, -9) for p in pos][:B], dtype=torch.int32)
+        q = torch.randn(B, Hq, d, generator=g).cuda().to(DT[dtype])
+        k, v = (torch.randn(B, Hkv, d, generator=g).cuda().to(DT[dtype]) for _ in range(2))
+        wk, wv = kc.clone(), vc.clone()
+        # slots the sequence has not reached yet are never read
+        ik, iv = kc.clone(), vc.clone()
+        for b in range(B):
+            p = int(pos[b])
+            if p >= 0:
+                slot = p if p < sinks else sinks + (p - sinks) % window
+                wk[b, :, slot], wv[b, :, slot] = k[b], v[b]
+                ik[b, :, p + 1:], iv[b, :, p + 1:] = float("nan"), float("nan")
+                ik[b, :, slot], iv[b, :, slot] = float("nan"), float("nan")
+        out = mesa.swa_step(q, k, v, ik, iv, pos.cuda(), window=window, sinks=sinks)
+        for b in range(B):
+            p = int(pos[b])
+            if p < 0:
+                assert torch.count_nonzero(out[b]) == 0
+                assert torch.equal(ik[b], kc[b]) and torch.equal(iv[b], vc[b])
+                continue
+            n = min(p + 1, cap)
+            assert torch.equal(ik[b, :, :n], wk[b, :, :n]) and torch.equal(iv[b, :, :n], wv[b, :, :n])
+            assert torch.isnan(ik[b, :, n:]).all()
+            one = slice(b, b + 1)
+            want, bound = step_ref(q[one], wk[one], wv[one], pos[one], window, sinks, ref.matrix_path(q.dtype, d))
+            ref.check(out[one], want, bound, f"row {b}")
+        kc, vc = wk, wv
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128), ("bf16", 32)])
+def test_prompt_then_steps_follow_the_whole_sequence(mesa, dtype, d):
+    """forward on a prompt, cache_fill, then steps: the rows of one forward over everything."""
+    B, Hq, Hkv, P, N, window, sinks = 2, 6, 2, 75, 60, 40, 3
+    T = P + N
+    q, k, v, _ = inputs(B, Hq, Hkv, T, T, d, dtype, seed=12)
+    want = ref.swa(q, k, v, window, sinks, matrix=ref.matrix_path(q.dtype, d))["out"]
+    lens = torch.tensor([P, P - 30], dtype=torch.int32, device="cuda")       # a padded batch of prompts
+    kc = torch.full((B, Hkv, sinks + window, d), float("nan"), device="cuda", dtype=q.dtype)
+    vc = kc.clone()
+    mesa.swa_cache_fill(k[:, :, :P].contiguous(), v[:, :, :P].contiguous(), kc, vc, window=window, sinks=sinks, lens=lens)
+    for i in range(N):
+        at = lens.long() + i
+        rows = torch.arange(B, device="cuda")
+        out = mesa.swa_step(q[rows, :, at].contiguous(), k[rows, :, at].contiguous(), v[rows, :, at].contiguous(), kc, vc,
+                            at.int(), window=window, sinks=sinks)
+        ref.check(out, want[0][rows, :, at], want[1][rows, :, at], f"token {i}")
+
+
+@pytest.mark.parametrize("start,S", [(0, 1), (0, 9), (0, 10), (0, 47), (5, 3), (7, 30), (46, 4), (100, 1)])
+def test_cache_fill_is_the_steps(mesa, start, S):
+    window, sinks, d = 16, 5, 32
+    q, k, v, _ = inputs(3, 2, 2, S, S, d, "bf16", seed=S)
+    kc = torch.randn(3, 2, window + sinks, d, device="cuda").to(q.dtype)
+    vc = kc + 1
+    wk, wv = kc.clone(), vc.clone()
+    lens = torch.tensor([S, max(S - 3, 0), -2], dtype=torch.int32, device="cuda")
+    for i in range(S):
+        pos = torch.where(lens > i, start + i, -1).int()
+        mesa.swa_step(q[:, :, i].contiguous(), k[:, :, i].contiguous(), v[:, :, i].contiguous(), wk, wv, pos,
+                      window=window, sinks=sinks)
+    mesa.swa_cache_fill(k, v, kc, vc, window=window, sinks=sinks, start=start, lens=lens)
+    assert torch.equal(kc, wk) and torch.equal(vc, wv)
+
+
+def test_step_graph_follows_pos(mesa):
+    """One captured step replayed for a run of tokens: pos advances on the device."""
+    B, Hq, Hkv, d, window, sinks = 2, 4, 2, 128, 20, 2
+    T = 50
+    q, k, v, _ = inputs(B, Hq, Hkv, T, T, d, "bf16", seed=14)
+    want = ref.swa(q, k, v, window, sinks, matrix=True)["out"]
+    kc, vc = (torch.zeros(B, Hkv, window + sinks, d, device="cuda", dtype=q.dtype) for _ in range(2))
+    qi, ki, vi = q[:, :, 0].clone(), k[:, :, 0].clone(), v[:, :, 0].clone()
+    pos = torch.zeros(B, dtype=torch.int32, device="cuda")
+    mesa.swa_step(qi, ki, vi, kc, vc, pos, window=window, sinks=sinks)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = mesa.swa_step(qi, ki, vi, kc, vc, pos, window=window, sinks=sinks)
+        pos.add_(1)
+    for t in range(T):
+        for dst, src in ((qi, q), (ki, k), (vi, v)):
+            dst.copy_(src[:, :, t])
+        graph.replay()
+        ref.check(out, want[0][:, :, t], want[1][:, :, t], f"token {t}")
+
+
+def test_cache_past_32_bit_offsets(mesa):
+    """The last head of caches of more than 2^31 elements."""
+    B, Hkv, d, window, sinks = 2, 2, 128, (1 << 22) + 3, 4
+    cap = window + sinks
+    assert B * Hkv * cap * d > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(15)
+    kc, vc = (torch.empty(B, Hkv, cap, d, device="cuda", dtype=torch.bfloat16).normal_(generator=g) for _ in range(2))
+    q = torch.randn(B, Hkv, d, generator=g, device="cuda").bfloat16()
+    k, v = (torch.randn(B, Hkv, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    pos = torch.tensor([cap - 1, 2 * cap - sinks - 1], dtype=torch.int32, device="cuda")
+    out = mesa.swa_step(q, k, v, kc, vc, pos, window=window, sinks=sinks)
+    assert torch.equal(kc[0, :, cap - 1], k[0])
+    one = slice(1, 2)
+    want, bound = ref.swa(q[one, 1:, None], kc[one, 1:], vc[one, 1:], cap, 0, matrix=True)["out"]
+    ref.check(out[one, 1:], want[:, :, 0], bound[:, :, 0], "out")
+
+
+def test_step_refusals(mesa):
+    q, k, v, _ = inputs(2, 4, 2, 1, 1, 64, "bf16")
+    q, k, v = q[:, :, 0].contiguous(), k[:, :, 0].contiguous(), v[:, :, 0].contiguous()
+    kc, vc = (torch.zeros(2, 2, 12, 64, device="cuda", dtype=q.dtype) for _ in range(2))
+    pos = torch.zeros(2, dtype=torch.int32, device="cuda")
+    mesa.swa_step(q, k, v, kc, vc, pos, window=10, sinks=2)
+    with pytest.raises(ValueError):
+        mesa.swa_step(q, k, v, kc, vc, pos, window=10, sinks=3)
+    with pytest.raises(TypeError):
+        mesa.swa_step(q, k, v, kc, vc, pos.long(), window=10, sinks=2)
+    with pytest.raises(ValueError):
+        mesa.swa_step(q, k, v, kc, vc, pos.cpu(), window=10, sinks=2)
+    with pytest.raises(ValueError):
+        mesa.swa_step(q, k, v, kc[:, :, ::2], vc, pos, window=10, sinks=2)
+    with pytest.raises(mesa.MesaError) as e:
+        mesa.swa_step(q, k, v, kc, kc, pos, window=10, sinks=2)
+    assert e.value.status == 1
