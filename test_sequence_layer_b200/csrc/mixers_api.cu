@@ -168,7 +168,7 @@ mesa_status mesa_swa_forward(const void* q, const void* k, const void* v, int B,
     if (clash({{out, nq}, {lse, (size_t)B * Hq * T * 4}}, {{q, nq}, {k, nk}, {v, nk}})) return MESA_ERR_INVALID_ARG;
     SwaArgs a{q, k, v, B, Hq, Hkv, T, S, d, window < S ? window : S, sinks, scale, dtype, out, lse};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return status(swa_forward_simt(a, st));
+    return status(swa_tc_supported(d, dtype) ? swa_forward_tc(a, st) : swa_forward_simt(a, st));
 }
 
 size_t mesa_swa_backward_workspace_size(int B, int Hq, int Hkv, int T, int S, int d, int sinks, mesa_dtype dtype) {

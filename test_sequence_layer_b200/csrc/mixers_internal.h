@@ -60,6 +60,9 @@ struct SwaBackwardArgs {
     void* dv;
     void* workspace;
 };
+// tensor cores: bf16, d = 64 or 128 (swa_tc_forward.cu)
+bool swa_tc_supported(int d, mesa_dtype dtype);
+cudaError_t swa_forward_tc(const SwaArgs& a, cudaStream_t st);
 cudaError_t swa_forward_simt(const SwaArgs& a, cudaStream_t st);
 cudaError_t swa_backward_simt(const SwaBackwardArgs& a, cudaStream_t st);
 // delta [B,Hq,T] = rowsum(dout * out)

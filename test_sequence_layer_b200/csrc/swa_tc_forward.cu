@@ -1,0 +1,339 @@
+// swa_tc_forward.cu -- sliding-window attention forward on the tensor cores
+// (bf16, d = 64 or 128).
+//
+// A CTA owns two tiles of 128 queries and walks the 128-key tiles that either
+// may see: the sink tile, then the window. The pair is two heads that share
+// keys where the group allows it, else two consecutive tiles of one head, so
+// that every key tile fetched serves two products. One warp issues the tile
+// copies, one the products, and four warps per query tile do the softmax, one
+// thread per row. Tensor memory holds S0, S1, O0, O1 (128 columns each); P
+// replaces the front half of its S as the bf16 left operand of P V.
+//
+// The products are issued in the order PV0(n) S0(n+1) PV1(n) S1(n+1): while
+// one tile's softmax runs, the tensor pipe works for the other.
+// The running maximum m of a row is only a reference for the exponents. It
+// moves when a score passes it by more than 8 (log2 units), and only then are
+// O and l rescaled: P stays below 2^8, which costs bf16 and fp32 nothing.
+// P is rounded to bf16 for its product with v; the sum l adds it unrounded.
+#include "swa_tc.cuh"
+
+namespace mesa {
+
+using namespace tc;
+
+namespace swa {
+
+bool make_map(CUtensorMap* m, const void* base, int d, int rows, int heads, int box_rows) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)d * 2 * rows};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, one[3] = {1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace swa
+
+namespace {
+
+constexpr int kQ = 128, kK = 128;                    // rows of a query and of a key tile
+constexpr int kSoftmaxThreads = 256;
+constexpr int kFwdThreads = kSoftmaxThreads + 64;
+
+template <int D> struct FwdSmem {
+    static constexpr int kTile = 128 * D * 2;        // bytes of one operand tile
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int oQ = 0;                     // two query tiles
+    static constexpr int oRing = 2 * kTile;          // K and V tiles, in turn
+    static constexpr int oBar = oRing + kStages * kTile;
+    static constexpr int bytes = oBar + (2 * kStages + 8) * 8 + 16 + 1024;   // + slack to align the base
+};
+
+struct FwdParams {
+    SwaArgs a;
+    int pair_heads;      // 1: the two tiles are heads 2 i, 2 i + 1 of one group; 0: consecutive tiles of one head
+    unsigned* err;
+};
+
+// One query tile as every role of the CTA sees it.
+struct QueryTile {
+    int head, t0, p0, p1;                            // flat query head, first query, first and last position
+    bool live;
+    __device__ __forceinline__ QueryTile(const FwdParams& f, int x) {
+        const int blk = blockIdx.x, y = blockIdx.y;
+        head = f.pair_heads ? 2 * y + x : y;
+        t0 = (f.pair_heads ? blk : 2 * blk + x) * kQ;
+        live = t0 < f.a.T;
+        p0 = f.a.S - f.a.T + t0;
+        p1 = f.a.S - f.a.T + min(t0 + kQ, f.a.T) - 1;
+    }
+    __device__ __forceinline__ bool uses(int j0, int window, int sinks) const {
+        return live && j0 <= p1 && (j0 + kK > p0 - window + 1 || j0 < sinks);
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv, const FwdParams f) {
+    using L = FwdSmem<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::oBar);
+    uint64_t* empty = full + L::kStages;
+    uint64_t* bar_q = empty + L::kStages;
+    uint64_t* s_full = bar_q + 1;                    // [2] scores of tile x are in tensor memory
+    uint64_t* p_full = s_full + 2;                   // [2] weights of tile x are
+    uint64_t* o_full = p_full + 2;                   // all products done
+    uint32_t* slot = reinterpret_cast<uint32_t*>(o_full + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const SwaArgs& a = f.a;
+    const QueryTile q0(f, 0), q1(f, 1);
+    const swa::KeyTiles kt(q0.p0, q1.live ? q1.p1 : q0.p1, a.window, a.sinks, kK);
+    const int hkv = q0.head / (a.Hq / a.Hkv);        // heads of one sequence follow one another: also flat
+
+    if (tid == 0) {
+        for (int i = 0; i < L::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(bar_q, 1);
+        mbar_init(o_full, 1);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&s_full[x], 1);
+            mbar_init(&p_full[x], 128);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 8) tmem_alloc(slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = *slot;
+    const uint32_t tS[2] = {tm, tm + 128}, tO[2] = {tm + 256, tm + 384};
+    bool ok = true;
+
+    if (warp == 8) {
+        if (lane == 0) {
+            // ---- copies: the query tiles, then K and V of every key tile ----
+            mbar_arrive_expect_tx(bar_q, 2 * L::kTile);
+            for (int x = 0; x < 2; ++x) {
+                const QueryTile& q = x ? q1 : q0;
+                for (int c = 0; c < D / 64; ++c)
+                    swa::tma_load(smem + L::oQ + x * L::kTile + c * 16384, &mq, c * 64, q.t0, q.head, bar_q);
+            }
+            for (int i = 0; i < 2 * kt.n && ok; ++i) {
+                const int st = i % L::kStages;
+                ok = mbar_wait(&empty[st], ((i / L::kStages) & 1) ^ 1);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&full[st], L::kTile);
+                for (int c = 0; c < D / 64; ++c)
+                    swa::tma_load(smem + L::oRing + st * L::kTile + c * 16384, (i & 1) ? &mv : &mk, c * 64,
+                                  kt.tile(i >> 1) * kK, hkv, &full[st]);
+            }
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            // ---- products ----
+            constexpr uint32_t idS = swa::idesc_bf16(128, 128, false, false);
+            constexpr uint32_t idO = swa::idesc_bf16(128, D, false, true);
+            const uint32_t sq = smem_addr(smem + L::oQ), sr = smem_addr(smem + L::oRing);
+            uint32_t np[2] = {0, 0};                 // weights taken so far, per tile
+            auto wait_full = [&](int i) { return mbar_wait(&full[i % L::kStages], (i / L::kStages) & 1); };
+            auto scores = [&](int x, int it) {
+                const uint32_t k = sr + (2 * it % L::kStages) * L::kTile, q = sq + x * L::kTile;
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t o = (s / 4) * 16384 + (s % 4) * 32;
+                    mma_f16(tS[x], sdesc(q + o, 0, 1024), sdesc(k + o, 0, 1024), idS, s > 0);
+                }
+                mma_commit(&s_full[x]);
+            };
+            auto values = [&](int x, int it) {
+                const uint32_t v = sr + ((2 * it + 1) % L::kStages) * L::kTile;
+#pragma unroll
+                for (int s = 0; s < kK / 16; ++s)
+                    swa::mma_ts(tO[x], tS[x] + 8 * s, sdesc(v + s * 2048, 16384, 1024), idO, np[x] > 0 || s > 0);
+                ++np[x];
+            };
+            ok = mbar_wait(bar_q, 0) && wait_full(0);
+            if (ok) {
+                const int j = kt.tile(0) * kK;
+                if (q0.uses(j, a.window, a.sinks)) scores(0, 0);
+                if (q1.uses(j, a.window, a.sinks)) scores(1, 0);
+                mma_commit(&empty[0]);
+            }
+            for (int it = 0; it < kt.n && ok; ++it) {
+                const int j = kt.tile(it) * kK, jn = kt.tile(it + 1) * kK;
+                const bool more = it + 1 < kt.n;
+                ok = wait_full(2 * it + 1);
+                for (int x = 0; x < 2 && ok; ++x) {
+                    const QueryTile& q = x ? q1 : q0;
+                    if (q.uses(j, a.window, a.sinks)) {
+                        ok = mbar_wait(&p_full[x], np[x] & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        values(x, it);
+                    }
+                    if (x == 1) mma_commit(&empty[(2 * it + 1) % L::kStages]);
+                    if (!more) continue;
+                    if (x == 0) ok = wait_full(2 * it + 2);
+                    if (ok && q.uses(jn, a.window, a.sinks)) scores(x, it + 1);
+                    if (ok && x == 1) mma_commit(&empty[(2 * it + 2) % L::kStages]);
+                }
+            }
+            mma_commit(o_full);
+            // leave only when nothing is in flight any more
+            mbar_wait(o_full, 0);
+        }
+    } else {
+        // ---- softmax of tile x, one row per thread ----
+        const int x = warp >> 2;
+        const QueryTile& q = x ? q1 : q0;
+        const int row = (warp & 3) * 32 + lane, pos = q.p0 + row;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const float sc = a.scale * swa::kLog2e, slack = 8.f / sc;
+        float m = -INFINITY;
+        float2 l2 = make_float2(0.f, 0.f);
+        uint32_t n = 0;
+        for (int it = 0; it < kt.n; ++it) {
+            const int j0 = kt.tile(it) * kK;
+            if (!q.uses(j0, a.window, a.sinks)) continue;
+            ok = mbar_wait(&s_full[x], n & 1);
+            if (!ok) break;
+            tc_fence_after();
+            float s[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32_x32(tS[x] + lanes + 32 * c, s[c]);
+            tmem_wait_ld();
+            const bool whole = j0 + kK - 1 <= q.p0 && q.p0 + kQ - 1 - j0 < a.window;
+            if (!whole) {
+                const int hi = pos - j0, lo = pos - a.window + 1 - j0, sk = a.sinks - j0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int j = 32 * c + e;
+                        if (!(j <= hi && (j >= lo || j < sk))) s[c][e] = -INFINITY;
+                    }
+            }
+            float mx[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                mx[c] = fmaxf(s[c][0], s[c][1]);
+#pragma unroll
+                for (int e = 2; e < 32; e += 2) mx[c] = fmaxf(mx[c], fmaxf(s[c][e], s[c][e + 1]));
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            float keep = 1.f;
+            if (m == -INFINITY) {
+                m = top;                             // O and l hold nothing yet
+            } else if (top > m + slack) {
+                keep = swa::ex2((m - top) * sc);
+                m = top;
+            }
+            if (__any_sync(~0u, keep != 1.f)) {
+                // S(n) is complete, so P V(n - 1), issued before it, is too
+                l2.x *= keep;
+                l2.y *= keep;
+#pragma unroll
+                for (int c = 0; c < D; c += 16) {
+                    float o[16];
+                    tmem_ld32_x16(tO[x] + lanes + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] *= keep;
+                    tmem_st32_x16(tO[x] + lanes + c, o);
+                }
+            }
+            const float neg = m == -INFINITY ? 0.f : -m * sc;
+            const float2 sc2 = make_float2(sc, sc), neg2 = make_float2(neg, neg);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float pk[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    float2 v = swa::fma2(make_float2(s[c][e], s[c][e + 1]), sc2, neg2);
+                    v.x = swa::ex2(v.x);
+                    v.y = swa::ex2(v.y);
+                    l2 = swa::add2(l2, v);
+                    pk[e / 2] = __uint_as_float(swa::pack_bf16(v.x, v.y));
+                }
+                tmem_st32_x16(tS[x] + lanes + 16 * c, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            swa::mbar_arrive(&p_full[x]);
+            ++n;
+        }
+        // ---- output ----
+        if (ok && q.live) {
+            ok = mbar_wait(o_full, 0);
+            tc_fence_after();
+            const int t = q.t0 + row;
+            const bool in = t < a.T;
+            const float l = l2.x + l2.y, inv = 1.f / l;
+            const size_t r = (size_t)q.head * a.T + t;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32_x32(tO[x] + lanes + c, o);
+                tmem_wait_ld();
+                if (in && ok) {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + r * D + c);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        dst[e / 8] = make_uint4(swa::pack_bf16(o[e] * inv, o[e + 1] * inv),
+                                                swa::pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                                                swa::pack_bf16(o[e + 4] * inv, o[e + 5] * inv),
+                                                swa::pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+                }
+            }
+            if (in && ok && a.lse) a.lse[r] = fmaf(m, a.scale, logf(l));
+            tc_fence_before();
+        }
+    }
+    if (!ok) record_error(f.err, kErrTimeout);
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tm, 512);
+}
+
+template <int D>
+cudaError_t launch(const SwaArgs& a, cudaStream_t st) {
+    using L = FwdSmem<D>;
+    CUtensorMap mq, mk, mv;
+    if (!swa::make_map(&mq, a.q, D, a.T, a.B * a.Hq, kQ) || !swa::make_map(&mk, a.k, D, a.S, a.B * a.Hkv, kK) ||
+        !swa::make_map(&mv, a.v, D, a.S, a.B * a.Hkv, kK))
+        return cudaErrorInvalidValue;
+    FwdParams f{a, (a.Hq / a.Hkv) % 2 == 0 ? 1 : 0, error_word_ptr()};
+    if (!f.err) return cudaErrorUnknown;
+    cudaError_t e = cudaFuncSetAttribute(swa_tc_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes);
+    if (e != cudaSuccess) return e;
+    const int tiles = (a.T + kQ - 1) / kQ;
+    const dim3 grid = f.pair_heads ? dim3(tiles, a.B * a.Hq / 2) : dim3((tiles + 1) / 2, a.B * a.Hq);
+    swa_tc_fwd_kernel<D><<<grid, kFwdThreads, L::bytes, st>>>(mq, mk, mv, f);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool swa_tc_supported(int d, mesa_dtype dtype) { return dtype == MESA_BF16 && (d == 64 || d == 128); }
+
+cudaError_t swa_forward_tc(const SwaArgs& a, cudaStream_t st) {
+    LaunchTimer lt(kKindSwa, st);
+    return a.d == 128 ? launch<128>(a, st) : launch<64>(a, st);
+}
+
+}  // namespace mesa
