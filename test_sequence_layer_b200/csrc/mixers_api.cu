@@ -173,7 +173,7 @@ mesa_status mesa_swa_forward(const void* q, const void* k, const void* v, int B,
 
 size_t mesa_swa_backward_workspace_size(int B, int Hq, int Hkv, int T, int S, int d, int sinks, mesa_dtype dtype) {
     if (swa_shape(B, Hq, Hkv, d, 1, sinks, 1.f, dtype) != MESA_OK || swa_lengths(T, S) != MESA_OK) return 0;
-    return delta_bytes(B, Hq, T);
+    return swa_tc_supported(d, dtype) ? swa_tc_workspace_bytes(B, Hq, Hkv, T, d, sinks) : delta_bytes(B, Hq, T);
 }
 
 mesa_status mesa_swa_backward(const void* q, const void* k, const void* v, const void* out, const float* lse,
@@ -202,7 +202,7 @@ mesa_status mesa_swa_backward(const void* q, const void* k, const void* v, const
     SwaArgs f{q, k, v, B, Hq, Hkv, T, S, d, window < S ? window : S, sinks, scale, dtype,
               const_cast<void*>(out), const_cast<float*>(lse)};
     SwaBackwardArgs a{f, dout, dq, dk, dv, workspace};
-    return status(swa_backward_simt(a, st));
+    return status(swa_tc_supported(d, dtype) ? swa_backward_tc(a, st) : swa_backward_simt(a, st));
 }
 
 mesa_status mesa_swa_step(const void* q, const void* k, const void* v, void* k_cache, void* v_cache,

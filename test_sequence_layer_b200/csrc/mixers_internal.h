@@ -65,6 +65,9 @@ bool swa_tc_supported(int d, mesa_dtype dtype);
 cudaError_t swa_forward_tc(const SwaArgs& a, cudaStream_t st);
 cudaError_t swa_forward_simt(const SwaArgs& a, cudaStream_t st);
 cudaError_t swa_backward_simt(const SwaBackwardArgs& a, cudaStream_t st);
+// tensor cores (swa_tc_backward.cu)
+size_t swa_tc_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int sinks);
+cudaError_t swa_backward_tc(const SwaBackwardArgs& a, cudaStream_t st);
 // delta [B,Hq,T] = rowsum(dout * out)
 cudaError_t swa_delta(const SwaArgs& a, const void* dout, float* delta, cudaStream_t st);
 
