@@ -3,24 +3,19 @@
 //   r = sigmoid(ga), i = sigmoid(gx), la = -8 softplus(lambda) r, a = e^la,
 //   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t
 //
-// A CTA owns 32 VEC channels of one sequence (a lane holds VEC of them, so a
-// warp reads whole 64- or 128-byte rows) and walks time in tiles. Inside a
-// tile each warp takes a run of tokens: it forms a and b of its run once, in
-// registers, reduces them to the run's map h -> A h + Hl, and after one
-// barrier every thread composes the maps of the runs before its own and
-// rescans its registers. Nothing is read or computed twice. The next tile's
-// rows are loaded into registers before the barrier, which keeps 48 (forward)
-// or 32 (backward) 128-byte rows per warp in flight.
-// Where channels alone do not fill the GPU, a cluster of 2 to 8 CTAs shares a
-// sequence: CTA r takes tiles r, r + n, ..., and per round the CTAs exchange
-// their tiles' maps through distributed shared memory.
-#include <cooperative_groups.h>
-
-#include "mesa_common.cuh"
-#include "mesa_internal.h"
-#include "mixers_internal.h"
-
-namespace cg = cooperative_groups;
+// A CTA owns 32 VEC channels of one sequence (a lane holds VEC of them) and
+// walks time in tiles of 64 tokens. Inside a tile each of eight warps takes a
+// run of eight tokens: it forms a and b of its run, reduces them to the run's
+// map h -> A h + Hl, and after one barrier every thread composes the maps of
+// the runs before its own and rescans its registers. Each row is read once.
+// Tiles arrive in shared memory two ahead (one thread issues tensor copies;
+// widths a tensor copy cannot take use 4-byte asynchronous copies, odd bf16
+// widths plain loads), so registers are left for the run.
+// A cluster of up to 16 CTAs shares a sequence: CTA r takes tiles r, r + n,
+// ..., and per round every CTA sends its tile's map to the others with
+// asynchronous remote stores that count on the receiver's mbarrier, so no CTA
+// waits for more than the maps themselves.
+#include "swa_tc.cuh"
 
 namespace mesa {
 namespace {
@@ -68,11 +63,9 @@ template <> struct Row<__nv_bfloat16, 2> {
 };
 
 // ---- arithmetic on VEC channels: packed fp32 pairs where there are two ----
-__device__ __forceinline__ float ex2(float v) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
-    return y;
-}
+using swa::ex2;
+using swa::kLog2e;
+constexpr float kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ float rcp(float v) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
@@ -133,7 +126,6 @@ template <int VEC, float (*F)(float)> __device__ __forceinline__ V<VEC> each(V<V
     return a;
 }
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kTiny = 1e-36f;      // a normal number: keeps rsqrt finite where 1 - a^2 = 0
 
 // 1 - e^(2 la) from la2 = la log2 e <= 0 and a: below t = -2 la = 1/4 by the
@@ -177,152 +169,259 @@ __device__ __forceinline__ void gates(V<VEC> x, V<VEC> ga, V<VEC> gx, V<VEC> k2,
     b = W::mul(W::mul(x, m2), each<VEC, rsq>(s));
 }
 
-// ---- forward ----
-constexpr int kFwdSeg = 16;                     // tokens per warp and tile
-constexpr int kFwdTile = kWarps * kFwdSeg;      // 128
-static_assert(kFwdTile == 2 * kLruSave, "a forward tile saves two states");
+// ---- tiles and the maps between them ----
+constexpr int kSeg = 8;                         // tokens per warp and tile
+constexpr int kTile = kWarps * kSeg;
+static_assert(kTile == kLruSave, "a tile starts at a saved state");
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads, 2) lru_forward_kernel(LruArgs p, int groups, int ncta) {
+enum Load { kTensor, kAsync4, kPlain };
+
+// NT input tensors of a CTA's channels, two tiles ahead in shared memory.
+// Words of 4 bytes, [stage][tensor][token][lane]: a lane's VEC channels.
+template <typename T, int VEC, int NT, int LOAD> struct Stager {
+    using R = Row<T, VEC>;
+    static constexpr int kStageBytes = NT * kTile * 32 * 4;
+    static constexpr int kBytes = LOAD == kPlain ? 0 : 2 * kStageBytes;
+    const CUtensorMap* maps[NT];
+    const T* src[NT];                           // the CTA's sequence, at this lane's channels
+    uint32_t* buf;
+    uint64_t* full;                             // [2]
+    int T_, D, c_cta, b;
+    bool live;
+
+    // rounds up to 2 ahead; call by all threads, tile < 0 or past the end: nothing to load
+    __device__ __forceinline__ void issue(int round, int tile, int tiles) {
+        if (tile < 0 || tile >= tiles) return;
+        const int st = round & 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (LOAD == kTensor) {
+            if (threadIdx.x == 0) {
+                tc::mbar_arrive_expect_tx(&full[st], kStageBytes);
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    swa::tma_load(buf + (st * NT + i) * kTile * 32, maps[i], c_cta, tile * kTile, b, &full[st]);
+            }
+        } else if (LOAD == kAsync4) {
+            const int t0 = tile * kTile + warp * kSeg;
+#pragma unroll
+            for (int s = 0; s < kSeg; ++s)
+                if (live && t0 + s < T_) {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_addr(
+                                         buf + ((st * NT + i) * kTile + warp * kSeg + s) * 32 + lane)),
+                                     "l"(src[i] + (size_t)(t0 + s) * D)
+                                     : "memory");
+                }
+        }
+        if (LOAD == kAsync4) asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // the tile of this round has landed; `ahead`: one more tile is on its way
+    __device__ __forceinline__ bool wait(int round, bool ahead) {
+        if (LOAD == kTensor) return tc::mbar_wait(&full[round & 1], (round >> 1) & 1);
+        if (LOAD == kAsync4) {
+            if (ahead) asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        return true;
+    }
+    __device__ __forceinline__ typename R::Raw get(int round, int i, int tile, int s) const {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (LOAD == kPlain) {
+            const int t = tile * kTile + warp * kSeg + s;
+            return live && t < T_ ? R::load(src[i], (size_t)t * D) : R::zero();
+        }
+        const uint32_t w = buf[(((round & 1) * NT + i) * kTile + warp * kSeg + s) * 32 + lane];
+        return *reinterpret_cast<const typename R::Raw*>(&w);
+    }
+};
+
+// maps x -> v.x * x + v.y per channel, exchanged between the CTAs of a cluster
+template <int VEC> struct Exchange {
+    float2* peer;                               // [2][ncta][VEC][32]
+    uint64_t* bar;                              // [2]
+    int ncta, rank;
+    // by one warp: this CTA's map to every CTA of the cluster, itself included
+    __device__ __forceinline__ void send(int round, const float2 (&m)[VEC]) {
+        const int par = round & 1, lane = threadIdx.x & 31;
+        if (lane == 0) tc::mbar_arrive_expect_tx(&bar[par], ncta * VEC * 32 * 8);
+        __syncwarp();
+        const uint32_t b0 = tc::smem_addr(&bar[par]);
+        for (int r = 0; r < ncta; ++r) {
+            uint32_t rb;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(b0), "r"(r));
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                uint32_t ra;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;"
+                    : "=r"(ra)
+                    : "r"(tc::smem_addr(&peer[((par * ncta + rank) * VEC + e) * 32 + lane])), "r"(r));
+                asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(ra),
+                             "f"(m[e].x), "f"(m[e].y), "r"(rb)
+                             : "memory");
+            }
+        }
+    }
+    __device__ __forceinline__ bool wait(int round) { return tc::mbar_wait(&bar[round & 1], (round >> 1) & 1); }
+    __device__ __forceinline__ float2 get(int round, int r, int e) const {
+        return peer[(((round & 1) * ncta + r) * VEC + e) * 32 + (threadIdx.x & 31)];
+    }
+};
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+struct Where {
+    int rank, b, c0, c_cta, tiles, rounds;
+    bool live;
+    size_t base;
+    template <int VEC> __device__ __forceinline__ static Where make(const LruArgs& p, int groups, int ncta) {
+        Where w;
+        w.rank = ncta > 1 ? blockIdx.x % ncta : 0;
+        const unsigned work = blockIdx.x / ncta;
+        w.b = work / groups;
+        w.c_cta = (work % groups) * (32 * VEC);
+        w.c0 = w.c_cta + (threadIdx.x & 31) * VEC;
+        w.live = w.c0 < p.D;                    // VEC divides D
+        w.base = (size_t)w.b * p.T * p.D + w.c0;
+        w.tiles = (p.T + kTile - 1) / kTile;
+        w.rounds = (w.tiles + ncta - 1) / ncta;
+        return w;
+    }
+};
+
+template <int VEC> __host__ __device__ constexpr int peer_bytes(int ncta) { return ncta > 1 ? 2 * ncta * VEC * 32 * 8 : 0; }
+
+// ---- forward ----
+template <typename T, int VEC, int LOAD>
+__global__ void __launch_bounds__(kThreads, 3)
+lru_forward_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap ma,
+                   const __grid_constant__ CUtensorMap mg, LruArgs p, int groups, int ncta, unsigned* err) {
     using R = Row<T, VEC>;
     using W = V<VEC>;
+    using St = Stager<T, VEC, 3, LOAD>;
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float2 seg[2][kWarps][VEC][32];
-    __shared__ float2 peer[2][kLruMaxCluster][VEC][32];
-    const int rank = ncta > 1 ? blockIdx.x % ncta : 0;
-    const unsigned work = blockIdx.x / ncta;
-    const int b = work / groups;
+    __shared__ uint64_t bars[4];
+    const Where w = Where::make<VEC>(p, groups, ncta);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c0 = (work % groups) * (32 * VEC) + lane * VEC;
-    const bool live = c0 < p.D;                 // VEC divides D
-    const size_t base = (size_t)b * p.T * p.D + c0;
-    const int tiles = (p.T + kFwdTile - 1) / kFwdTile;
-    const int rounds = (tiles + ncta - 1) / ncta;
+    St in{{&mx, &ma, &mg},
+          {static_cast<const T*>(p.x) + w.base, static_cast<const T*>(p.ga) + w.base, static_cast<const T*>(p.gx) + w.base},
+          reinterpret_cast<uint32_t*>(smem), bars, p.T, p.D, w.c_cta, w.b, w.live};
+    Exchange<VEC> ex{reinterpret_cast<float2*>(smem + St::kBytes), bars + 2, ncta, w.rank};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 4; ++i) tc::mbar_init(&bars[i], 1);
+        tc::fence_mbar_init();
+    }
+    if (ncta > 1) cluster_sync(); else __syncthreads();
+    bool ok = true;
 
     W k2, carry;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-        k2.v[e] = live ? -kC * kLog2e * softplus(p.lambda[c0 + e]) : 0.f;
-        carry.v[e] = live && p.h0 ? p.h0[(size_t)b * p.D + c0 + e] : 0.f;
+        k2.v[e] = w.live ? -kC * kLog2e * softplus(p.lambda[w.c0 + e]) : 0.f;
+        carry.v[e] = w.live && p.h0 ? p.h0[(size_t)w.b * p.D + w.c0 + e] : 0.f;
     }
-    typename R::Raw rx[kFwdSeg], ra[kFwdSeg], rg[kFwdSeg];
-    // tokens past the end get a closed gate: a = 1 and b = 0 exactly
-    auto fetch = [&](int tile) {
-        const long long t0 = (long long)tile * kFwdTile + warp * kFwdSeg;
-        const size_t o = base + (size_t)t0 * p.D;
-        const T* x = static_cast<const T*>(p.x) + o;
-        const T* ga = static_cast<const T*>(p.ga) + o;
-        const T* gx = static_cast<const T*>(p.gx) + o;
-        if (live && t0 + kFwdSeg <= p.T) {
+    in.issue(0, w.rank, w.tiles);
+    in.issue(1, w.rank + ncta, w.tiles);
+    for (int j = 0; j < w.rounds; ++j) {
+        const int tile = j * ncta + w.rank, par = j & 1;
+        const int t0 = tile * kTile + warp * kSeg;
+        const bool any = tile < w.tiles;
+        W a[kSeg], h[kSeg], A = W::all(1.f), Hl = W::all(0.f);
+        if (any && ok) ok = in.wait(j, tile + ncta < w.tiles);
 #pragma unroll
-            for (int s = 0; s < kFwdSeg; ++s) {
-                rx[s] = R::load(x, (size_t)s * p.D);
-                ra[s] = R::load(ga, (size_t)s * p.D);
-                rg[s] = R::load(gx, (size_t)s * p.D);
-            }
-        } else {
-#pragma unroll
-            for (int s = 0; s < kFwdSeg; ++s) {
-                const bool in = live && t0 + s < p.T;
-                rx[s] = in ? R::load(x, (size_t)s * p.D) : R::zero();
-                ra[s] = in ? R::load(ga, (size_t)s * p.D) : R::closed();
-                rg[s] = in ? R::load(gx, (size_t)s * p.D) : R::zero();
-            }
-        }
-    };
-    fetch(rank);
-    for (int j = 0; j < rounds; ++j) {
-        const int tile = j * ncta + rank, par = j & 1;
-        const long long t0 = (long long)tile * kFwdTile + warp * kFwdSeg;
-        W a[kFwdSeg], h[kFwdSeg], A = W::all(1.f), Hl = W::all(0.f);
-#pragma unroll
-        for (int s = 0; s < kFwdSeg; ++s) {
+        for (int s = 0; s < kSeg; ++s) {
             W x, ga, gx;
-            R::unpack(rx[s], x.v);
-            R::unpack(ra[s], ga.v);
-            R::unpack(rg[s], gx.v);
+            R::unpack(in.get(j, 0, tile, s), x.v);
+            R::unpack(in.get(j, 1, tile, s), ga.v);
+            R::unpack(in.get(j, 2, tile, s), gx.v);
             gates<VEC>(x, ga, gx, k2, a[s], h[s]);
+        }
+        if (t0 + kSeg > p.T) {                   // tokens past the end change nothing
+#pragma unroll
+            for (int s = 0; s < kSeg; ++s)
+                if (t0 + s >= p.T) a[s] = W::all(1.f), h[s] = W::all(0.f);
+        }
+#pragma unroll
+        for (int s = 0; s < kSeg; ++s) {
             Hl = W::fma(a[s], Hl, h[s]);
             A = W::mul(A, a[s]);
         }
-        if (j + 1 < rounds) fetch(tile + ncta);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) seg[par][warp][e][lane] = make_float2(A.v[e], Hl.v[e]);
         __syncthreads();
+        in.issue(j, tile + 2 * ncta, w.tiles);   // every thread has read the stage
+        W hv;
         if (ncta > 1) {
-            cg::cluster_group cl = cg::this_cluster();
-            // this tile's map goes to every CTA of the cluster, one warp each
-            if (warp < ncta) {
+            if (warp == 0) {
                 float2 m[VEC];
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     m[e] = make_float2(1.f, 0.f);
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) {
-                        const float2 g = seg[par][w][e][lane];
+                    for (int u = 0; u < kWarps; ++u) {
+                        const float2 g = seg[par][u][e][lane];
                         m[e].y = fmaf(g.x, m[e].y, g.y);
                         m[e].x *= g.x;
                     }
                 }
-                for (int r = warp; r < ncta; r += kWarps) {
-                    float2* dst = cl.map_shared_rank(&peer[par][rank][0][0], r);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) dst[e * 32 + lane] = m[e];
-                }
+                ex.send(j, m);
             }
-            cl.sync();
-        }
-        W hv;
+            if (ok) ok = ex.wait(j);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            float c = carry.v[e];
-            hv.v[e] = c;
-            if (ncta > 1) {
+            for (int e = 0; e < VEC; ++e) {
+                float c = carry.v[e];
                 for (int r = 0; r < ncta; ++r) {
-                    if (r == rank) hv.v[e] = c;
-                    const float2 m = peer[par][r][e][lane];
+                    if (r == w.rank) hv.v[e] = c;
+                    const float2 m = ex.get(j, r, e);
                     c = fmaf(m.x, c, m.y);
                 }
                 carry.v[e] = c;
-                for (int w = 0; w < warp; ++w) {
-                    const float2 m = seg[par][w][e][lane];
+                for (int u = 0; u < warp; ++u) {
+                    const float2 m = seg[par][u][e][lane];
                     hv.v[e] = fmaf(m.x, hv.v[e], m.y);
                 }
-            } else {
+            }
+        } else {
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    if (w == warp) hv.v[e] = c;
-                    const float2 m = seg[par][w][e][lane];
+            for (int e = 0; e < VEC; ++e) {
+                float c = carry.v[e];
+#pragma unroll
+                for (int u = 0; u < kWarps; ++u) {
+                    if (u == warp) hv.v[e] = c;
+                    const float2 m = seg[par][u][e][lane];
                     c = fmaf(m.x, c, m.y);
                 }
                 carry.v[e] = c;
             }
         }
-        if (p.saved && live && (warp * kFwdSeg) % kLruSave == 0 && t0 < p.T) {
-            const size_t row = (size_t)b * ((p.T + kLruSave - 1) / kLruSave) + t0 / kLruSave;
+        if (p.saved && w.live && warp == 0 && any) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) p.saved[row * p.D + c0 + e] = hv.v[e];
+            for (int e = 0; e < VEC; ++e) p.saved[((size_t)w.b * w.tiles + tile) * p.D + w.c0 + e] = hv.v[e];
         }
-        if (p.y && live) {
-            T* y = static_cast<T*>(p.y) + base + (size_t)t0 * p.D;
-            if (t0 + kFwdSeg <= p.T) {
+        if (p.y && w.live) {
+            T* y = static_cast<T*>(p.y) + w.base + (size_t)t0 * p.D;
+            if (t0 + kSeg <= p.T) {
 #pragma unroll
-                for (int s = 0; s < kFwdSeg; ++s) {
+                for (int s = 0; s < kSeg; ++s) {
                     hv = W::fma(a[s], hv, h[s]);
                     R::store(y, (size_t)s * p.D, hv.v);
                 }
             } else {
 #pragma unroll
-                for (int s = 0; s < kFwdSeg; ++s) {
+                for (int s = 0; s < kSeg; ++s) {
                     hv = W::fma(a[s], hv, h[s]);
                     if (t0 + s < p.T) R::store(y, (size_t)s * p.D, hv.v);
                 }
             }
         }
     }
-    if (p.hT && live && rank == 0 && warp == 0) {
+    if (p.hT && w.live && w.rank == 0 && warp == 0) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) p.hT[(size_t)b * p.D + c0 + e] = carry.v[e];
+        for (int e = 0; e < VEC; ++e) p.hT[(size_t)w.b * p.D + w.c0 + e] = carry.v[e];
     }
+    if (!ok) record_error(err, kErrTimeout);
 }
 
 // ---- backward ----
@@ -331,69 +430,76 @@ __global__ void __launch_bounds__(kThreads, 2) lru_forward_kernel(LruArgs p, int
 // state before it, so the tiles only pass c on. s = dL/dlog a * log a feeds
 // both dgate_a = s (1 - r) and dlambda. Registers bound the tile: a, r, i and
 // g of a run are kept, b and sqrt(1 - a^2) are formed again in the last pass.
-constexpr int kBwdSeg = 8;
-constexpr int kBwdTile = kWarps * kBwdSeg;
-static_assert(kBwdTile == kLruSave, "a backward tile starts at a saved state");
-
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads, 2) lru_backward_kernel(LruBackwardArgs q, int groups, int ncta) {
+template <typename T, int VEC, int LOAD>
+__global__ void __launch_bounds__(kThreads, 2)
+lru_backward_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap ma,
+                    const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap md, LruBackwardArgs q,
+                    int groups, int ncta, unsigned* err) {
     using R = Row<T, VEC>;
     using W = V<VEC>;
+    using St = Stager<T, VEC, 4, LOAD>;
     const LruArgs& p = q.f;
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float2 segh[2][kWarps][VEC][32];               // A, Hl of a run
     __shared__ float segc[2][kWarps][VEC][32];                // Cl of a run
-    __shared__ float2 peer[2][kLruMaxCluster][VEC][32];
     __shared__ float red[kWarps][VEC][32];
-    const int rank = ncta > 1 ? blockIdx.x % ncta : 0;
-    const unsigned work = blockIdx.x / ncta;
-    const int b = work / groups;
+    __shared__ uint64_t bars[4];
+    const Where w = Where::make<VEC>(p, groups, ncta);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c0 = (work % groups) * (32 * VEC) + lane * VEC;
-    const bool live = c0 < p.D;
-    const size_t base = (size_t)b * p.T * p.D + c0;
-    const int tiles = (p.T + kBwdTile - 1) / kBwdTile;
-    const int rounds = (tiles + ncta - 1) / ncta;
+    St in{{&mx, &ma, &mg, &md},
+          {static_cast<const T*>(p.x) + w.base, static_cast<const T*>(p.ga) + w.base, static_cast<const T*>(p.gx) + w.base,
+           static_cast<const T*>(q.dy) + w.base},
+          reinterpret_cast<uint32_t*>(smem), bars, p.T, p.D, w.c_cta, w.b, w.live};
+    Exchange<VEC> ex{reinterpret_cast<float2*>(smem + St::kBytes), bars + 2, ncta, w.rank};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 4; ++i) tc::mbar_init(&bars[i], 1);
+        tc::fence_mbar_init();
+    }
+    if (ncta > 1) cluster_sync(); else __syncthreads();
+    bool ok = true;
 
     W k2, carry, acc = W::all(0.f);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-        k2.v[e] = live ? -kC * kLog2e * softplus(p.lambda[c0 + e]) : 0.f;
-        carry.v[e] = live && q.dhT ? q.dhT[(size_t)b * p.D + c0 + e] : 0.f;
+        k2.v[e] = w.live ? -kC * kLog2e * softplus(p.lambda[w.c0 + e]) : 0.f;
+        carry.v[e] = w.live && q.dhT ? q.dhT[(size_t)w.b * p.D + w.c0 + e] : 0.f;
     }
-    typename R::Raw rx[kBwdSeg], ra[kBwdSeg], rg[kBwdSeg], rd[kBwdSeg];
-    W hs;
     // tile numbers run down from the last; tiles below 0 (a cluster's last
     // round) are empty: closed gates and no gradient
-    auto fetch = [&](int tile) {
-        const long long t0 = (long long)tile * kBwdTile + warp * kBwdSeg;
-#pragma unroll
-        for (int s = 0; s < kBwdSeg; ++s) {
-            const bool in = live && tile >= 0 && t0 + s < p.T;
-            const size_t o = base + (size_t)(t0 + s) * p.D;
-            rx[s] = in ? R::load(p.x, o) : R::zero();
-            ra[s] = in ? R::load(p.ga, o) : R::closed();
-            rg[s] = in ? R::load(p.gx, o) : R::zero();
-            rd[s] = in ? R::load(q.dy, o) : R::zero();
-        }
+    const int top = w.tiles - 1 - w.rank;
+    auto state = [&](int tile) {
+        W s;
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
-            hs.v[e] = live && tile >= 0 ? p.saved[((size_t)b * tiles + tile) * p.D + c0 + e] : 0.f;
+            s.v[e] = w.live && tile >= 0 ? p.saved[((size_t)w.b * w.tiles + tile) * p.D + w.c0 + e] : 0.f;
+        return s;
     };
-    fetch(tiles - 1 - rank);
-    for (int j = 0; j < rounds; ++j) {
-        const int tile = tiles - 1 - (j * ncta + rank), par = j & 1;
-        const long long t0 = (long long)tile * kBwdTile + warp * kBwdSeg;
-        W a[kBwdSeg], r[kBwdSeg], iv[kBwdSeg], g[kBwdSeg];
-        typename R::Raw xk[kBwdSeg];
+    in.issue(0, top, w.tiles);
+    in.issue(1, top - ncta, w.tiles);
+    W hs = state(top);
+    for (int j = 0; j < w.rounds; ++j) {
+        const int tile = top - j * ncta, par = j & 1;
+        const int t0 = tile * kTile + warp * kSeg;
+        const bool any = tile >= 0;
+        W a[kSeg], r[kSeg], iv[kSeg], g[kSeg];
+        typename R::Raw xk[kSeg];
         W A = W::all(1.f), Hl = W::all(0.f), Cl = W::all(0.f), hv = hs;
+        hs = state(tile - ncta);
+        if (any && ok) ok = in.wait(j, tile - ncta >= 0);
+        const bool tail = !any || t0 + kSeg > p.T;
 #pragma unroll
-        for (int s = 0; s < kBwdSeg; ++s) {
+        for (int s = 0; s < kSeg; ++s) {
             W x, ga, gx;
-            xk[s] = rx[s];
-            R::unpack(rx[s], x.v);
-            R::unpack(ra[s], ga.v);
-            R::unpack(rg[s], gx.v);
-            R::unpack(rd[s], g[s].v);
+            xk[s] = in.get(j, 0, tile, s);
+            typename R::Raw ra = in.get(j, 1, tile, s), rg = in.get(j, 2, tile, s), rd = in.get(j, 3, tile, s);
+            if (tail && (!any || t0 + s >= p.T)) {
+                xk[s] = rg = rd = R::zero();
+                ra = R::closed();
+            }
+            R::unpack(xk[s], x.v);
+            R::unpack(ra, ga.v);
+            R::unpack(rg, gx.v);
+            R::unpack(rd, g[s].v);
             r[s] = each<VEC, rcp>(one_plus_exp<VEC>(ga));
             iv[s] = each<VEC, rcp>(one_plus_exp<VEC>(gx));
             const W la2 = W::mul(k2, r[s]);
@@ -404,74 +510,71 @@ __global__ void __launch_bounds__(kThreads, 2) lru_backward_kernel(LruBackwardAr
             A = W::mul(A, a[s]);
         }
 #pragma unroll
-        for (int s = kBwdSeg - 1; s >= 0; --s) Cl = W::mul(a[s], W::add(g[s], Cl));
-        if (j + 1 < rounds) fetch(tile - ncta);
+        for (int s = kSeg - 1; s >= 0; --s) Cl = W::mul(a[s], W::add(g[s], Cl));
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             segh[par][warp][e][lane] = make_float2(A.v[e], Hl.v[e]);
             segc[par][warp][e][lane] = Cl.v[e];
         }
         __syncthreads();
+        in.issue(j, tile - 2 * ncta, w.tiles);
+        W gc;
         if (ncta > 1) {
-            cg::cluster_group cl = cg::this_cluster();
-            if (warp < ncta) {
+            if (warp == 0) {
                 float2 m[VEC];
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     m[e] = make_float2(1.f, 0.f);
 #pragma unroll
-                    for (int w = kWarps - 1; w >= 0; --w) {
-                        const float A1 = segh[par][w][e][lane].x;
-                        m[e].y = fmaf(A1, m[e].y, segc[par][w][e][lane]);
+                    for (int u = kWarps - 1; u >= 0; --u) {
+                        const float A1 = segh[par][u][e][lane].x;
+                        m[e].y = fmaf(A1, m[e].y, segc[par][u][e][lane]);
                         m[e].x *= A1;
                     }
                 }
-                for (int t = warp; t < ncta; t += kWarps) {
-                    float2* dst = cl.map_shared_rank(&peer[par][rank][0][0], t);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) dst[e * 32 + lane] = m[e];
-                }
+                ex.send(j, m);
             }
-            cl.sync();
+            if (ok) ok = ex.wait(j);
         }
-        W gc;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             float c = carry.v[e];
             if (ncta > 1) {
                 float mine = c;
                 for (int t = 0; t < ncta; ++t) {
-                    if (t == rank) mine = c;
-                    const float2 m = peer[par][t][e][lane];
+                    if (t == w.rank) mine = c;
+                    const float2 m = ex.get(j, t, e);
                     c = fmaf(m.x, c, m.y);
                 }
                 carry.v[e] = c;
                 c = mine;
-                for (int w = kWarps - 1; w > warp; --w) c = fmaf(segh[par][w][e][lane].x, c, segc[par][w][e][lane]);
+                for (int u = kWarps - 1; u > warp; --u) c = fmaf(segh[par][u][e][lane].x, c, segc[par][u][e][lane]);
                 gc.v[e] = c;
             } else {
-                gc.v[e] = c;
 #pragma unroll
-                for (int w = kWarps - 1; w >= 0; --w) {
-                    if (w == warp) gc.v[e] = c;
-                    c = fmaf(segh[par][w][e][lane].x, c, segc[par][w][e][lane]);
+                for (int u = kWarps - 1; u >= 0; --u) {
+                    if (u == warp) gc.v[e] = c;
+                    c = fmaf(segh[par][u][e][lane].x, c, segc[par][u][e][lane]);
                 }
                 carry.v[e] = c;
             }
-            for (int w = 0; w < warp; ++w) {
-                const float2 m = segh[par][w][e][lane];
+            for (int u = 0; u < warp; ++u) {
+                const float2 m = segh[par][u][e][lane];
                 hv.v[e] = fmaf(m.x, hv.v[e], m.y);
             }
         }
 #pragma unroll
-        for (int s = kBwdSeg - 1; s >= 0; --s) {
+        for (int s = kSeg - 1; s >= 0; --s) {
             g[s] = W::add(g[s], gc);
             gc = W::mul(a[s], g[s]);
         }
         W part = W::all(0.f);
-        const bool tail = !live || tile < 0 || t0 + kBwdSeg > p.T;
+        const size_t o0 = w.base + (size_t)t0 * p.D;
+        T* pdx = static_cast<T*>(q.dx) + o0;
+        T* pda = static_cast<T*>(q.dga) + o0;
+        T* pdg = static_cast<T*>(q.dgx) + o0;
 #pragma unroll
-        for (int s = 0; s < kBwdSeg; ++s) {
+        for (int s = 0; s < kSeg; ++s) {
             W x;
             R::unpack(xk[s], x.v);
             const W la2 = W::mul(k2, r[s]), la = W::mul(la2, W::all(kLn2));
@@ -488,11 +591,10 @@ __global__ void __launch_bounds__(kThreads, 2) lru_backward_kernel(LruBackwardAr
             const W dgx = W::fma(W::mul(gb, W::all(-1.f)), iv[s], gb);
             part = W::add(part, sv);
             hv = W::fma(a[s], hv, bb);
-            if (!tail || (live && tile >= 0 && t0 + s < p.T)) {
-                const size_t o = base + (size_t)(t0 + s) * p.D;
-                R::store(q.dx, o, dx.v);
-                R::store(q.dga, o, dga.v);
-                R::store(q.dgx, o, dgx.v);
+            if (w.live && (!tail || (any && t0 + s < p.T))) {
+                R::store(pdx, (size_t)s * p.D, dx.v);
+                R::store(pda, (size_t)s * p.D, dga.v);
+                R::store(pdg, (size_t)s * p.D, dgx.v);
             }
         }
         acc = W::add(acc, part);
@@ -500,16 +602,17 @@ __global__ void __launch_bounds__(kThreads, 2) lru_backward_kernel(LruBackwardAr
 #pragma unroll
     for (int e = 0; e < VEC; ++e) red[warp][e][lane] = acc.v[e];
     __syncthreads();
-    if (warp == 0 && live) {
+    if (warp == 0 && w.live) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) s += red[w][e][lane];
-            q.partial[((size_t)b * ncta + rank) * p.D + c0 + e] = s;
-            if (q.dh0 && rank == 0) q.dh0[(size_t)b * p.D + c0 + e] = carry.v[e];
+            for (int u = 0; u < kWarps; ++u) s += red[u][e][lane];
+            q.partial[((size_t)w.b * ncta + w.rank) * p.D + w.c0 + e] = s;
+            if (q.dh0 && w.rank == 0) q.dh0[(size_t)w.b * p.D + w.c0 + e] = carry.v[e];
         }
     }
+    if (!ok) record_error(err, kErrTimeout);
 }
 
 // dlambda = sigmoid(lambda) / softplus(lambda) * sum over rows of partial
@@ -553,26 +656,39 @@ __global__ void lru_step_kernel(const void* x, const void* ga, const void* gx, c
     R::store(y, i, h.v);
 }
 
-bool pair_ok(int D, std::initializer_list<const void*> ps) {
-    if (D % 2) return false;
+bool all_aligned(std::initializer_list<const void*> ps, uintptr_t n) {
     for (const void* q : ps)
-        if (reinterpret_cast<uintptr_t>(q) % 4) return false;
+        if (reinterpret_cast<uintptr_t>(q) % n) return false;
     return true;
 }
+bool pair_ok(int D, std::initializer_list<const void*> ps) { return D % 2 == 0 && all_aligned(ps, 4); }
 
-// CTAs per sequence and channel group: doubled while the grid is below two
-// CTAs per SM and every CTA still gets a tile.
+// [B][T][D] as a 3-D map of tiles of 64 tokens by 128 bytes of channels
+bool channel_map(CUtensorMap* m, const LruArgs& a, const void* base) {
+    const bool f32 = a.dtype == MESA_F32;
+    return swa::encode_map(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f32 ? 4 : 2, base,
+                           a.D, a.T, a.B, f32 ? 32 : 64, kTile, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// CTAs per sequence and channel group. Eight where every CTA still walks four
+// tiles: many short CTAs leave the SMs evenly loaded. Sixteen if the grid
+// would otherwise not give every SM two.
 int cluster_size(long long blocks, int tiles) {
     int n = 1;
-    while (n < kLruMaxCluster && blocks * n < 2 * 148 && tiles >= 2 * n) n *= 2;
+    while (n < 8 && tiles >= 8 * n && blocks * n < 16 * 148) n *= 2;
+    while (n < kLruMaxCluster && tiles >= 2 * n && blocks * n < 2 * 148) n *= 2;
     return n;
 }
 
 template <typename F, typename... A>
-cudaError_t launch_cluster(F* kernel, unsigned grid, int ncta, cudaStream_t st, A... args) {
+cudaError_t launch_cluster(F* kernel, unsigned grid, int ncta, int smem, cudaStream_t st, A... args) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && ncta > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -587,50 +703,80 @@ struct Plan {
     int groups, ncta;
     unsigned grid;
 };
-Plan plan(int B, int T, int D, int vec, int tile) {
+Plan plan(int B, int T, int D, int vec) {
     Plan pl;
     pl.groups = (D + 32 * vec - 1) / (32 * vec);
     const long long blocks = (long long)B * pl.groups;
-    pl.ncta = cluster_size(blocks, (T + tile - 1) / tile);
+    pl.ncta = cluster_size(blocks, (T + kTile - 1) / kTile);
     pl.grid = (unsigned)(blocks * pl.ncta);
     return pl;
+}
+
+template <typename T, int VEC, int LOAD>
+cudaError_t forward(const LruArgs& a, const CUtensorMap (&m)[4], unsigned* err, cudaStream_t st) {
+    const Plan pl = plan(a.B, a.T, a.D, VEC);
+    return launch_cluster(lru_forward_kernel<T, VEC, LOAD>, pl.grid, pl.ncta,
+                          Stager<T, VEC, 3, LOAD>::kBytes + peer_bytes<VEC>(pl.ncta), st, m[0], m[1], m[2], a, pl.groups,
+                          pl.ncta, err);
+}
+
+template <typename T, int VEC, int LOAD>
+cudaError_t backward(const LruBackwardArgs& q, const CUtensorMap (&m)[4], unsigned* err, cudaStream_t st) {
+    const LruArgs& a = q.f;
+    const Plan pl = plan(a.B, a.T, a.D, VEC);
+    cudaError_t e = launch_cluster(lru_backward_kernel<T, VEC, LOAD>, pl.grid, pl.ncta,
+                                   Stager<T, VEC, 4, LOAD>::kBytes + peer_bytes<VEC>(pl.ncta), st, m[0], m[1], m[2], m[3],
+                                   q, pl.groups, pl.ncta, err);
+    if (e != cudaSuccess) return e;
+    lru_dlambda_kernel<<<(a.D + 31) / 32, dim3(32, 8), 0, st>>>(q.partial, (size_t)a.B * pl.ncta, a.D, a.lambda,
+                                                               q.dlambda);
+    return cudaGetLastError();
+}
+
+// whether tensor copies can take these rows: 16-byte bases and row lengths
+bool tensor_ok(const LruArgs& a, std::initializer_list<const void*> ps) {
+    return (size_t)a.D * (a.dtype == MESA_F32 ? 4 : 2) % 16 == 0 && all_aligned(ps, 16);
 }
 
 }  // namespace
 
 size_t lru_backward_rows(int B, int T) {
-    const int t = (T + kBwdTile - 1) / kBwdTile;          // a CTA of a cluster has a tile
+    const int t = (T + kTile - 1) / kTile;                // a CTA of a cluster has a tile
     return (size_t)B * (t < 1 ? 1 : t < kLruMaxCluster ? t : kLruMaxCluster);
 }
 
 cudaError_t lru_forward(const LruArgs& a, cudaStream_t st) {
     LaunchTimer lt(kKindLru, st);
-    const bool pair = a.dtype == MESA_BF16 && pair_ok(a.D, {a.x, a.ga, a.gx, a.y});
-    const Plan pl = plan(a.B, a.T, a.D, pair ? 2 : 1, kFwdTile);
-    if (a.dtype == MESA_F32) return launch_cluster(lru_forward_kernel<float, 1>, pl.grid, pl.ncta, st, a, pl.groups, pl.ncta);
-    if (pair) return launch_cluster(lru_forward_kernel<__nv_bfloat16, 2>, pl.grid, pl.ncta, st, a, pl.groups, pl.ncta);
-    return launch_cluster(lru_forward_kernel<__nv_bfloat16, 1>, pl.grid, pl.ncta, st, a, pl.groups, pl.ncta);
+    unsigned* err = error_word_ptr();
+    if (!err) return cudaErrorUnknown;
+    CUtensorMap m[4] = {};
+    using bf = __nv_bfloat16;
+    if (tensor_ok(a, {a.x, a.ga, a.gx}) && all_aligned({a.y}, 4)) {
+        if (!channel_map(&m[0], a, a.x) || !channel_map(&m[1], a, a.ga) || !channel_map(&m[2], a, a.gx))
+            return cudaErrorInvalidValue;
+        return a.dtype == MESA_F32 ? forward<float, 1, kTensor>(a, m, err, st) : forward<bf, 2, kTensor>(a, m, err, st);
+    }
+    if (a.dtype == MESA_F32) return forward<float, 1, kAsync4>(a, m, err, st);
+    return pair_ok(a.D, {a.x, a.ga, a.gx, a.y}) ? forward<bf, 2, kAsync4>(a, m, err, st)
+                                                : forward<bf, 1, kPlain>(a, m, err, st);
 }
 
 cudaError_t lru_backward(const LruBackwardArgs& q, cudaStream_t st) {
-    const LruArgs& a = q.f;
-    const bool pair = a.dtype == MESA_BF16 && pair_ok(a.D, {a.x, a.ga, a.gx, q.dy, q.dx, q.dga, q.dgx});
-    const Plan pl = plan(a.B, a.T, a.D, pair ? 2 : 1, kBwdTile);
-    cudaError_t e;
-    {
-        LaunchTimer lt(kKindLruBwd, st);
-        if (a.dtype == MESA_F32)
-            e = launch_cluster(lru_backward_kernel<float, 1>, pl.grid, pl.ncta, st, q, pl.groups, pl.ncta);
-        else if (pair)
-            e = launch_cluster(lru_backward_kernel<__nv_bfloat16, 2>, pl.grid, pl.ncta, st, q, pl.groups, pl.ncta);
-        else
-            e = launch_cluster(lru_backward_kernel<__nv_bfloat16, 1>, pl.grid, pl.ncta, st, q, pl.groups, pl.ncta);
-    }
-    if (e != cudaSuccess) return e;
     LaunchTimer lt(kKindLruBwd, st);
-    lru_dlambda_kernel<<<(a.D + 31) / 32, dim3(32, 8), 0, st>>>(q.partial, (size_t)a.B * pl.ncta, a.D, a.lambda,
-                                                               q.dlambda);
-    return cudaGetLastError();
+    const LruArgs& a = q.f;
+    unsigned* err = error_word_ptr();
+    if (!err) return cudaErrorUnknown;
+    CUtensorMap m[4] = {};
+    using bf = __nv_bfloat16;
+    if (tensor_ok(a, {a.x, a.ga, a.gx, q.dy}) && all_aligned({q.dx, q.dga, q.dgx}, 4)) {
+        if (!channel_map(&m[0], a, a.x) || !channel_map(&m[1], a, a.ga) || !channel_map(&m[2], a, a.gx) ||
+            !channel_map(&m[3], a, q.dy))
+            return cudaErrorInvalidValue;
+        return a.dtype == MESA_F32 ? backward<float, 1, kTensor>(q, m, err, st) : backward<bf, 2, kTensor>(q, m, err, st);
+    }
+    if (a.dtype == MESA_F32) return backward<float, 1, kAsync4>(q, m, err, st);
+    return pair_ok(a.D, {a.x, a.ga, a.gx, q.dy, q.dx, q.dga, q.dgx}) ? backward<bf, 2, kAsync4>(q, m, err, st)
+                                                                     : backward<bf, 1, kPlain>(q, m, err, st);
 }
 
 cudaError_t lru_step(const void* x, const void* ga, const void* gx, const float* lambda, int B, int D,

@@ -11,7 +11,7 @@
 namespace mesa {
 
 constexpr int kLruSave = 64;       // tokens between saved states
-constexpr int kLruMaxCluster = 8;  // CTAs that share one sequence's time axis
+constexpr int kLruMaxCluster = 16;  // CTAs that share one sequence's time axis
 
 struct LruArgs {
     const void* x;

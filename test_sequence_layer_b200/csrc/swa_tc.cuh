@@ -80,8 +80,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// bf16 [heads][rows][d] as a 3-D map of 64 x box_rows tiles, 128-byte swizzle;
-// rows past the end read as zeros.
+// A contiguous [z][y][x] tensor as a 3-D map of bx x by tiles; what lies past
+// an end reads as zeros.
+bool encode_map(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, const void* base, int x, int y, int z, int bx,
+                int by, CUtensorMapSwizzle swizzle);
+// bf16 [heads][rows][d] in tiles of 64 x box_rows, 128-byte swizzle
 bool make_map(CUtensorMap* m, const void* base, int d, int rows, int heads, int box_rows);
 
 }  // namespace swa

@@ -23,7 +23,8 @@ using namespace tc;
 
 namespace swa {
 
-bool make_map(CUtensorMap* m, const void* base, int d, int rows, int heads, int box_rows) {
+bool encode_map(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, const void* base, int x, int y, int z, int bx,
+                int by, CUtensorMapSwizzle swizzle) {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -36,12 +37,16 @@ bool make_map(CUtensorMap* m, const void* base, int d, int rows, int heads, int 
         return reinterpret_cast<Encode>(f);
     }();
     if (!encode) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads};
-    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)d * 2 * rows};
-    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, one[3] = {1, 1, 1};
-    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t dims[3] = {(cuuint64_t)x, (cuuint64_t)y, (cuuint64_t)z};
+    const cuuint64_t strides[2] = {(cuuint64_t)x * elem_bytes, (cuuint64_t)x * elem_bytes * y};
+    const cuuint32_t box[3] = {(cuuint32_t)bx, (cuuint32_t)by, 1}, one[3] = {1, 1, 1};
+    return encode(m, type, 3, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_map(CUtensorMap* m, const void* base, int d, int rows, int heads, int box_rows) {
+    return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, d, rows, heads, 64, box_rows,
+                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace swa
