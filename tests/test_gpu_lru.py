@@ -73,6 +73,21 @@ def test_backward(mesa, B, T, D, dtype):
             assert torch.equal(o, o2), n
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_fast_decays(mesa, dtype):
+    """Channels from slow to total decay side by side (not one CTA of slow ones alone)."""
+    x, ga, gx, lam, dy, h0, dh = inputs(2, 210, 150, dtype, seed=21)
+    lam += torch.linspace(0.0, 12.0, 150, device="cuda")
+    y, hT, saved = mesa.lru_forward(x, ga, gx, lam, h0=h0, return_state=True, return_saved=True)
+    want, wT, ey, eT = ref.lru(x, ga, gx, lam, h0)
+    ref.check(y, want, ey, "y")
+    ref.check(hT, wT, eT, "h_T")
+    got = mesa.lru_backward(x, ga, gx, lam, dy, saved=saved, dh_T=dh)
+    want, bound = ref.lru_grads(x, ga, gx, lam, h0, dy, dh)
+    for n, o, w, b in zip(("dx", "dgate_a", "dgate_x", "dlam", "dh0"), got, want, bound):
+        ref.check(o, w, b, n)
+
+
 @pytest.mark.parametrize("D,shift", [(66, 1), (65, 0), (64, 1), (64, 2)])
 def test_alignment(mesa, D, shift):
     """Odd widths and bases that allow only single-element accesses."""
@@ -90,12 +105,15 @@ def test_alignment(mesa, D, shift):
     ref.check(y1, want[:, 0], ey[:, 0], "step")
 
 
+@pytest.mark.parametrize("lams", [(-120.0, -95.0, -60.0, -25.0, -15.0, -3.0, 0.0, 5.0, 60.0),
+                                  (-120.0, -95.0, -60.0, -25.0, -15.0, -8.0, -6.0, -5.0, -4.0)],
+                         ids=["any decay", "slow decays"])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_extreme_gates(mesa, dtype):
-    """Closed, open and saturated gates, decays from none to total."""
+def test_extreme_gates(mesa, dtype, lams):
+    """Closed, open and saturated gates; decays from none to total, or slow ones alone."""
     B, T = 1, 200
     vals = torch.tensor([-float("inf"), -90.0, -60.0, -30.0, -10.0, 0.0, 10.0, 40.0, 100.0, float("inf")])
-    lams = torch.tensor([-120.0, -95.0, -60.0, -25.0, -15.0, -3.0, 0.0, 5.0, 60.0])
+    lams = torch.tensor(lams)
     D = len(vals) * len(lams)
     x, ga, gx, lam, dy, h0, dh = inputs(B, T, D, dtype, seed=3)
     ga[:] = vals.repeat(len(lams)).to(ga)
