@@ -136,12 +136,16 @@ mesa_status mesa_swa_backward(const void* q, const void* k, const void* v, const
  *   k_cache, v_cache  [B,Hkv,sinks+window,d] in `dtype`, updated in place.
  *                     Slots not yet used are not read.
  *   pos               int32 [B], device memory (a captured call follows it).
- * All 16-byte aligned (pos 4). d, sinks, scale as above; window >= 1;
- * sinks + window < 2^31; B, Hkv <= 65535.
+ *   workspace         mesa_swa_step_workspace_size() bytes, 256-byte aligned
+ *                     (that may be 0: then it may be NULL). Calls sharing a
+ *                     workspace must not overlap.
+ * All others 16-byte aligned (pos 4). d, sinks, scale as above; window >= 1;
+ * sinks + window < 2^31; B * Hq <= 65535.
  */
+size_t mesa_swa_step_workspace_size(int B, int Hq, int Hkv, int d, int window, int sinks, mesa_dtype dtype);
 mesa_status mesa_swa_step(const void* q, const void* k, const void* v, void* k_cache, void* v_cache,
                           const int32_t* pos, int B, int Hq, int Hkv, int d, int window, int sinks, float scale,
-                          mesa_dtype dtype, void* out, void* stream);
+                          mesa_dtype dtype, void* out, void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * The rolling caches after the S tokens k, v [B,Hkv,S,d] at positions start,

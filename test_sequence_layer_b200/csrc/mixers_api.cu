@@ -68,6 +68,12 @@ mesa_status swa_lengths(int T, int S) {
     return MESA_OK;
 }
 
+mesa_status step_shape(int B, int Hq, int Hkv, int d, int window, int sinks, float scale, mesa_dtype dtype) {
+    const mesa_status s = swa_shape(B, Hq, Hkv, d, window, sinks, scale, dtype);
+    if (s != MESA_OK) return s;
+    return (long long)sinks + window > 0x7fffffffLL ? MESA_ERR_UNSUPPORTED : MESA_OK;
+}
+
 size_t delta_bytes(int B, int Hq, int T) { return round_up((size_t)B * Hq * T * 4, 256); }
 
 }  // namespace
@@ -205,18 +211,28 @@ mesa_status mesa_swa_backward(const void* q, const void* k, const void* v, const
     return status(swa_tc_supported(d, dtype) ? swa_backward_tc(a, st) : swa_backward_simt(a, st));
 }
 
+size_t mesa_swa_step_workspace_size(int B, int Hq, int Hkv, int d, int window, int sinks, mesa_dtype dtype) {
+    if (step_shape(B, Hq, Hkv, d, window, sinks, 1.f, dtype) != MESA_OK) return 0;
+    SwaStepArgs a{};
+    a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.d = d, a.window = window, a.sinks = sinks, a.dtype = dtype;
+    return round_up(swa_step_workspace_bytes(a), 256);
+}
+
 mesa_status mesa_swa_step(const void* q, const void* k, const void* v, void* k_cache, void* v_cache,
                           const int32_t* pos, int B, int Hq, int Hkv, int d, int window, int sinks, float scale,
-                          mesa_dtype dtype, void* out, void* stream) {
-    mesa_status s = swa_shape(B, Hq, Hkv, d, window, sinks, scale, dtype);
+                          mesa_dtype dtype, void* out, void* workspace, size_t ws_bytes, void* stream) {
+    mesa_status s = step_shape(B, Hq, Hkv, d, window, sinks, scale, dtype);
     if (s != MESA_OK) return s;
-    if ((long long)sinks + window > 0x7fffffffLL) return MESA_ERR_UNSUPPORTED;
     if (!given({q, k, v, k_cache, v_cache, out}, 16) || !given({pos}, 4)) return MESA_ERR_INVALID_ARG;
     const size_t es = elem_size(dtype), nq = (size_t)B * Hq * d * es, nk = (size_t)B * Hkv * d * es;
     const size_t nc = nk * ((size_t)sinks + window);
-    if (clash({{out, nq}, {k_cache, nc}, {v_cache, nc}}, {{q, nq}, {k, nk}, {v, nk}, {pos, (size_t)B * 4}}))
+    const size_t need = mesa_swa_step_workspace_size(B, Hq, Hkv, d, window, sinks, dtype);
+    if (need && (!workspace || ws_bytes < need)) return MESA_ERR_WORKSPACE;
+    if (need && !aligned(workspace, 256)) return MESA_ERR_INVALID_ARG;
+    if (clash({{out, nq}, {k_cache, nc}, {v_cache, nc}, {workspace, need}},
+              {{q, nq}, {k, nk}, {v, nk}, {pos, (size_t)B * 4}}))
         return MESA_ERR_INVALID_ARG;
-    return status(swa_step({q, k, v, k_cache, v_cache, pos, B, Hq, Hkv, d, window, sinks, scale, dtype, out},
+    return status(swa_step({q, k, v, k_cache, v_cache, pos, B, Hq, Hkv, d, window, sinks, scale, dtype, out, workspace},
                            static_cast<cudaStream_t>(stream)));
 }
 

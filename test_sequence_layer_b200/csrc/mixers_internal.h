@@ -82,7 +82,9 @@ struct SwaStepArgs {
     float scale;
     mesa_dtype dtype;
     void* out;
+    void* workspace;
 };
+size_t swa_step_workspace_bytes(const SwaStepArgs& a);        // sizes and type of a matter
 cudaError_t swa_step(const SwaStepArgs& a, cudaStream_t st);
 cudaError_t swa_cache_fill(const void* k, const void* v, void* kc, void* vc, const int32_t* lens, int B, int Hkv,
                            int S, int d, int window, int sinks, int start, mesa_dtype dtype, cudaStream_t st);

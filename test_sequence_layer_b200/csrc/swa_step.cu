@@ -1,11 +1,16 @@
 // swa_step.cu -- one decoded token of sliding-window attention over a rolling
 // cache (mesa_swa_step), and the cache after a prompt (mesa_swa_cache_fill).
 //
-// The cache's bytes bound the step, so its slots are split over the warps of a
-// cluster of CTAs (1 to 16), each warp with its own running maximum, sum and
-// output rows; the parts are joined once at the end, first in a CTA's shared
-// memory and then through distributed shared memory, so a step is one launch
-// without a workspace.
+// The cache's bytes bound the step, so its slots are split over many CTAs, each
+// warp with its own running maximum, sum and output rows. Two ways of joining:
+//   cluster  a cluster of 1 to 16 CTAs shares a head; the parts are joined
+//            through distributed shared memory, in one launch.
+//   stream   the runs of 64 slots of all sequences and heads, laid end to end,
+//            are cut into equal shares, one per resident CTA, whatever the
+//            sequences' lengths. A head that one CTA covers is written by it;
+//            the parts of the others go to the workspace and a second launch
+//            joins them. Few heads over a long cache reach every SM this way,
+//            and ragged batches leave none idle.
 //
 // The new token's rows are read from the arguments, not from the cache: their
 // slot is written by one CTA while others run, and nobody reads it.
@@ -61,10 +66,6 @@ __device__ __forceinline__ void join(Part<ROWS, D>& part, int splits, int rank, 
     }
     if (splits > 1) cl.sync();                             // no CTA leaves while its part may be read
 }
-
-struct Row {                                               // what a CTA needs to know of its sequence
-    int own, n;                                            // the token's slot, slots in use
-};
 
 // ---- fp32 on the CUDA cores: any type, d in {16, 32, 64, 128} ----
 constexpr int kSimtRows = 8, kSimtThreads = 128;
@@ -191,59 +192,69 @@ __device__ __forceinline__ uint4 ld16(const __nv_bfloat16* p) {
     return *reinterpret_cast<const uint4*>(p);
 }
 
-constexpr int kMmaWarps = 4, kMmaThreads = kMmaWarps * 32;
+// What a CTA needs to know of one head's cache.
+struct Head {
+    const __nv_bfloat16* q;      // first of its query heads
+    const __nv_bfloat16* kin;    // the token's rows
+    const __nv_bfloat16* vin;
+    __nv_bfloat16* kc;
+    __nv_bfloat16* vc;
+    int own, n, rows;            // the token's slot, slots in use, query heads
+};
 
-// ROWS = 8 or 16 heads of the group per CTA
 template <int ROWS, int D>
-__global__ void __launch_bounds__(kMmaThreads) swa_step_mma_kernel(SwaStepArgs p, int splits) {
+__device__ __forceinline__ Head head_of(const SwaStepArgs& p, int b, int hk, int hg, int pos) {
+    using bf = __nv_bfloat16;
+    const int G = p.Hq / p.Hkv, cap = p.sinks + p.window, h0 = hg * ROWS;
+    const size_t kv = ((size_t)b * p.Hkv + hk) * D;
+    Head h;
+    h.q = static_cast<const bf*>(p.q) + ((size_t)b * p.Hq + hk * G + h0) * D;
+    h.kin = static_cast<const bf*>(p.k) + kv;
+    h.vin = static_cast<const bf*>(p.v) + kv;
+    h.kc = static_cast<bf*>(p.kc) + kv * cap;
+    h.vc = static_cast<bf*>(p.vc) + kv * cap;
+    h.own = slot_of(pos, p.window, p.sinks);
+    h.n = pos < cap - 1 ? pos + 1 : cap;
+    h.rows = min(ROWS, G - h0);
+    return h;
+}
+
+template <int D> __device__ __forceinline__ void append(const Head& h) {
+    if (threadIdx.x < D / 8) {
+        reinterpret_cast<uint4*>(h.kc + (size_t)h.own * D)[threadIdx.x] = ld16(h.kin + threadIdx.x * 8);
+        reinterpret_cast<uint4*>(h.vc + (size_t)h.own * D)[threadIdx.x] = ld16(h.vin + threadIdx.x * 8);
+    }
+}
+
+// One warp's part of a head: 16 slots from s0, then every `stride` slots below
+// `end`. s0 < end or nothing.
+template <int ROWS, int D>
+__device__ __forceinline__ void warp_part(const Head& h, float sc, int s0, int stride, int end, Part<ROWS, D>& part) {
     constexpr int kPieces = D / 32;                        // 16-byte pieces of a K row per lane
     constexpr int kSets = D / 64;                          // 64-wide runs of d in a V row
     using bf = __nv_bfloat16;
-    extern __shared__ float4 smem4[];
-    Part<ROWS, D>* parts = reinterpret_cast<Part<ROWS, D>*>(smem4);      // one per warp
-    const int G = p.Hq / p.Hkv, hgroups = (G + ROWS - 1) / ROWS;
-    const int rank = blockIdx.x % splits, b = blockIdx.z, hk = blockIdx.y / hgroups;
-    const int h0 = (blockIdx.y % hgroups) * ROWS, rows = min(ROWS, G - h0);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-    bf* out = static_cast<bf*>(p.out) + ((size_t)b * p.Hq + hk * G + h0) * D;
-    const int pos = p.pos[b];
-    if (pos < 0) {
-        for (int i = rank * kMmaThreads + tid; i < rows * D; i += splits * kMmaThreads) out[i] = to_out<bf>(0.f);
-        return;
-    }
-    const int cap = p.sinks + p.window, own = slot_of(pos, p.window, p.sinks);
-    const int n = pos < cap - 1 ? pos + 1 : cap;
-    const bf* kin = static_cast<const bf*>(p.k) + ((size_t)b * p.Hkv + hk) * D;
-    const bf* vin = static_cast<const bf*>(p.v) + ((size_t)b * p.Hkv + hk) * D;
-    bf* kc = static_cast<bf*>(p.kc) + ((size_t)b * p.Hkv + hk) * cap * D;
-    bf* vc = static_cast<bf*>(p.vc) + ((size_t)b * p.Hkv + hk) * cap * D;
-    if (rank == 0 && h0 == 0 && tid < D / 8) {
-        reinterpret_cast<uint4*>(kc + (size_t)own * D)[tid] = ld16(kin + tid * 8);
-        reinterpret_cast<uint4*>(vc + (size_t)own * D)[tid] = ld16(vin + tid * 8);
-    }
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     // rows the token's own slot or no token holds come from the arguments (the latter at weight 0)
-    auto krow = [&](int slot) { return slot == own || slot >= n ? kin : kc + (size_t)slot * D; };
-    auto vrow = [&](int slot) { return slot == own || slot >= n ? vin : vc + (size_t)slot * D; };
+    auto krow = [&](int slot) { return slot == h.own || slot >= h.n ? h.kin : h.kc + (size_t)slot * D; };
+    auto vrow = [&](int slot) { return slot == h.own || slot >= h.n ? h.vin : h.vc + (size_t)slot * D; };
     uint4 kr[2][kPieces], vr[4][kSets];
-    auto fetch_k = [&](int s0) {
+    auto fetch_k = [&](int s) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const bf* r = krow(s0 + 8 * t + g);
+            const bf* r = krow(s + 8 * t + g);
 #pragma unroll
             for (int u = 0; u < kPieces; ++u) kr[t][u] = ld16(r + (c + 4 * u) * 8);
         }
     };
-    auto fetch_v = [&](int s0) {
+    auto fetch_v = [&](int s) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const bf* r = vrow(s0 + 2 * c + (i & 1) + 8 * (i >> 1));
+            const bf* r = vrow(s + 2 * c + (i & 1) + 8 * (i >> 1));
 #pragma unroll
             for (int u = 0; u < kSets; ++u) vr[i][u] = ld16(r + (g + 8 * u) * 8);
         }
     };
-    const int stride = splits * kMmaWarps * 16;
-    int s0 = (rank * kMmaWarps + warp) * 16;
-    if (s0 < n) {
+    if (s0 < end) {
         fetch_k(s0);
         fetch_v(s0);
     }
@@ -251,18 +262,17 @@ __global__ void __launch_bounds__(kMmaThreads) swa_step_mma_kernel(SwaStepArgs p
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
         const uint4 z = make_uint4(0, 0, 0, 0);
-        const bf* qr = static_cast<const bf*>(p.q) + ((size_t)b * p.Hq + hk * G + h0) * D + (c + 4 * u) * 8;
-        q0[u] = g < rows ? ld16(qr + (size_t)g * D) : z;
-        q1[u] = ROWS > 8 && g + 8 < rows ? ld16(qr + (size_t)(g + 8) * D) : z;
+        const bf* qr = h.q + (c + 4 * u) * 8;
+        q0[u] = g < h.rows ? ld16(qr + (size_t)g * D) : z;
+        q1[u] = ROWS > 8 && g + 8 < h.rows ? ld16(qr + (size_t)(g + 8) * D) : z;
     }
-    const float sc = p.scale * kLog2e;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float o[kSets * 8][4];
 #pragma unroll
     for (int i = 0; i < kSets * 8; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    for (; s0 < n; s0 += stride) {
+    for (; s0 < end; s0 += stride) {
         float s[2][4];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -274,7 +284,7 @@ __global__ void __launch_bounds__(kMmaThreads) swa_step_mma_kernel(SwaStepArgs p
                 mma_bf16(s[t], q0[u].z, q1[u].z, q0[u].w, q1[u].w, kr[t][u].z, kr[t][u].w);
             }
         }
-        const bool more = s0 + stride < n;
+        const bool more = s0 + stride < end;
         if (more) fetch_k(s0 + stride);
         uint32_t pa[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -283,7 +293,7 @@ __global__ void __launch_bounds__(kMmaThreads) swa_step_mma_kernel(SwaStepArgs p
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int slot = s0 + 8 * (i >> 1) + 2 * c + (i & 1);
-                v[i] = slot < n ? s[i >> 1][2 * r + (i & 1)] * sc : -INFINITY;
+                v[i] = slot < h.n ? s[i >> 1][2 * r + (i & 1)] * sc : -INFINITY;
                 mx = fmaxf(mx, v[i]);
             }
             mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
@@ -324,43 +334,243 @@ __global__ void __launch_bounds__(kMmaThreads) swa_step_mma_kernel(SwaStepArgs p
     for (int r = 0; r < (ROWS > 8 ? 2 : 1); ++r) {
         l[r] += __shfl_xor_sync(~0u, l[r], 1);
         l[r] += __shfl_xor_sync(~0u, l[r], 2);
-        Part<ROWS, D>& w = parts[warp];
         const int row = g + 8 * r;
-        if (c == 0) w.m[row] = m[r], w.l[row] = l[r];
+        if (c == 0) part.m[row] = m[r], part.l[row] = l[r];
 #pragma unroll
         for (int u = 0; u < kSets; ++u)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int j = 0; j < 8; j += 4)
-                    *reinterpret_cast<float4*>(&w.o[row][64 * u + 8 * (2 * c + e) + j]) =
+                    *reinterpret_cast<float4*>(&part.o[row][64 * u + 8 * (2 * c + e) + j]) =
                         make_float4(o[8 * u + j][2 * r + e], o[8 * u + j + 1][2 * r + e],
                                     o[8 * u + j + 2][2 * r + e], o[8 * u + j + 3][2 * r + e]);
     }
+}
+
+// Element (r, d) of the sum of `count` parts and, where it is asked for, their
+// common maximum and sum. A part without slots has m = -inf and weighs 0.
+template <int ROWS, int D, typename At>
+__device__ __forceinline__ float join_parts(At at, int count, int r, int d, float& m, float& l) {
+    m = -INFINITY;
+    for (int w = 0; w < count; ++w) m = fmaxf(m, at(w).m[r]);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float o = 0.f;
+    l = 0.f;
+    for (int w = 0; w < count; ++w) {
+        const Part<ROWS, D>& p = at(w);
+        const float f = exp2f(p.m[r] - ref);
+        o = fmaf(p.o[r][d], f, o);
+        l = fmaf(p.l[r], f, l);
+    }
+    return o;
+}
+
+constexpr int kMmaWarps = 4, kMmaThreads = kMmaWarps * 32, kRound = kMmaWarps * 16;
+
+// ROWS = 8 or 16 heads of the group per CTA
+template <int ROWS, int D>
+__global__ void __launch_bounds__(kMmaThreads, 3) swa_step_cluster_kernel(SwaStepArgs p, int splits) {
+    using bf = __nv_bfloat16;
+    extern __shared__ float4 smem4[];
+    Part<ROWS, D>* parts = reinterpret_cast<Part<ROWS, D>*>(smem4);      // one per warp, and their sum
+    const int G = p.Hq / p.Hkv, hgroups = (G + ROWS - 1) / ROWS;
+    const int rank = blockIdx.x % splits, b = blockIdx.z, hk = blockIdx.y / hgroups, hg = blockIdx.y % hgroups;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    bf* out = static_cast<bf*>(p.out) + ((size_t)b * p.Hq + hk * G + hg * ROWS) * D;
+    const int pos = p.pos[b], rows = min(ROWS, G - hg * ROWS);
+    if (pos < 0) {                                         // the same for the whole cluster
+        for (int i = rank * kMmaThreads + tid; i < rows * D; i += splits * kMmaThreads) out[i] = to_out<bf>(0.f);
+        return;
+    }
+    const Head h = head_of<ROWS, D>(p, b, hk, hg, pos);
+    if (rank == 0 && hg == 0) append<D>(h);
+    warp_part<ROWS, D>(h, p.scale * kLog2e, (rank * kMmaWarps + warp) * 16, splits * kRound, h.n, parts[warp]);
     __syncthreads();
-    // the warps' parts into the first one's place: each element by one thread
+    Part<ROWS, D>& sum = parts[kMmaWarps];
     for (int i = tid; i < rows * D; i += kMmaThreads) {
         const int r = i / D, d = i % D;
-        float mm = parts[0].m[r], v = 0.f;
+        float m, l;
+        sum.o[r][d] = join_parts<ROWS, D>([&](int w) -> const Part<ROWS, D>& { return parts[w]; }, kMmaWarps, r, d, m, l);
+        if (d == 0) sum.m[r] = m, sum.l[r] = l;
+    }
+    join<bf, ROWS, D>(sum, splits, rank, rows, out);
+}
+
+// ---- equal shares of all runs ----
+constexpr int kStreamCtas = 3 * 148;                       // all resident at once
+
+// Runs of kRound slots, numbered by sequence, then head, then slot. CTA i of n
+// (n at most half their number, so that few parts are short) takes [total i / n,
+// total (i + 1) / n). Its first head's part, if it shares it, goes to place 0 of
+// its two, its last to place 1.
+__device__ __forceinline__ int runs_of(int pos, int cap) {
+    return pos < 0 ? 0 : (int)(((long long)min(pos, cap - 1) + kRound) / kRound);
+}
+
+__device__ __forceinline__ long long shares(int ctas, long long total) {
+    return min((long long)ctas, (total + 1) / 2);
+}
+
+// Runs before sequence b and of all sequences (per head), by the whole block
+__device__ __forceinline__ void count_runs(const int32_t* pos, int B, int b, int cap, long long& before, long long& total) {
+    __shared__ long long s[2][32];
+    long long x = 0, y = 0;
+    for (int i = threadIdx.x; i < B; i += blockDim.x) {
+        const int r = runs_of(pos[i], cap);
+        y += r;
+        if (i < b) x += r;
+    }
 #pragma unroll
-        for (int w = 1; w < kMmaWarps; ++w) mm = fmaxf(mm, parts[w].m[r]);
-        const float ref = mm == -INFINITY ? 0.f : mm;        // a CTA without slots
-#pragma unroll
-        for (int w = 0; w < kMmaWarps; ++w) v = fmaf(parts[w].o[r][d], exp2f(parts[w].m[r] - ref), v);
-        parts[0].o[r][d] = v;
+    for (int k = 16; k; k >>= 1) {
+        x += __shfl_xor_sync(~0u, x, k);
+        y += __shfl_xor_sync(~0u, y, k);
     }
     __syncthreads();
-    if (tid < rows) {
-        float mm = parts[0].m[tid], v = 0.f;
+    if ((threadIdx.x & 31) == 0) s[0][threadIdx.x >> 5] = x, s[1][threadIdx.x >> 5] = y;
+    __syncthreads();
+    before = total = 0;
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) before += s[0][w], total += s[1][w];
+}
+
+template <int ROWS, int D>
+__global__ void __launch_bounds__(kMmaThreads, 3) swa_step_stream_kernel(SwaStepArgs p, Part<ROWS, D>* places) {
+    using bf = __nv_bfloat16;
+    extern __shared__ float4 smem4[];
+    Part<ROWS, D>* parts = reinterpret_cast<Part<ROWS, D>*>(smem4);
+    __shared__ int found[2];
+    const int G = p.Hq / p.Hkv, hgroups = (G + ROWS - 1) / ROWS, heads = p.Hkv * hgroups, cap = p.sinks + p.window;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    cudaTriggerProgrammaticLaunchCompletion();
+    long long none, total;
+    count_runs(p.pos, p.B, 0, cap, none, total);
+    total *= heads;
+    const long long n = shares(gridDim.x, total);
+    if (blockIdx.x >= n) return;
+    const long long lo = total * blockIdx.x / n, hi = total * (blockIdx.x + 1) / n;
+    // the sequence that holds run lo: warp 0 walks the lengths 32 at a time
+    __shared__ long long start;
+    if (warp == 0) {
+        long long base = 0;
+        for (int i = 0; i < p.B; i += 32) {
+            const long long r = i + lane < p.B ? (long long)runs_of(p.pos[i + lane], cap) * heads : 0;
+            long long inc = r;
 #pragma unroll
-        for (int w = 1; w < kMmaWarps; ++w) mm = fmaxf(mm, parts[w].m[tid]);
-        const float ref = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-        for (int w = 0; w < kMmaWarps; ++w) v = fmaf(parts[w].l[tid], exp2f(parts[w].m[tid] - ref), v);
-        parts[0].m[tid] = mm;
-        parts[0].l[tid] = v;
+            for (int k = 1; k < 32; k <<= 1) {
+                const long long t = __shfl_up_sync(~0u, inc, k);
+                if (lane >= k) inc += t;
+            }
+            const unsigned hit = __ballot_sync(~0u, base + inc > lo);
+            if (hit) {
+                if (lane == __ffs(hit) - 1) found[0] = i + lane, start = base + inc - r;
+                break;
+            }
+            base += __shfl_sync(~0u, inc, 31);
+        }
     }
-    join<bf, ROWS, D>(parts[0], splits, rank, rows, out);
+    __syncthreads();
+    int b = found[0];
+    long long at = lo, seq = start;
+    int pos = p.pos[b], runs = runs_of(pos, cap);
+    while (at < hi) {
+        if (at >= seq + (long long)runs * heads) {           // the next sequence that has any
+            seq += (long long)runs * heads;
+            pos = p.pos[++b];
+            runs = runs_of(pos, cap);
+            continue;
+        }
+        const int head = (int)((at - seq) / runs), r0 = (int)((at - seq) % runs);
+        const int r1 = (int)min((long long)runs, r0 + (hi - at));
+        const int hk = head / hgroups, hg = head % hgroups;
+        const Head h = head_of<ROWS, D>(p, b, hk, hg, pos);
+        if (hg == 0 && h.own / kRound >= r0 && h.own / kRound < r1) append<D>(h);
+        warp_part<ROWS, D>(h, p.scale * kLog2e, r0 * kRound + warp * 16, kRound, min(h.n, r1 * kRound), parts[warp]);
+        __syncthreads();
+        const bool whole = r0 == 0 && r1 == runs;
+        Part<ROWS, D>& place = places[2 * blockIdx.x + (at == lo ? 0 : 1)];
+        bf* out = static_cast<bf*>(p.out) + ((size_t)b * p.Hq + hk * G + hg * ROWS) * D;
+        for (int i = tid; i < h.rows * D; i += kMmaThreads) {
+            const int r = i / D, d = i % D;
+            float m, l;
+            const float o =
+                join_parts<ROWS, D>([&](int w) -> const Part<ROWS, D>& { return parts[w]; }, kMmaWarps, r, d, m, l);
+            if (whole) {
+                out[i] = to_out<bf>(o / l);
+            } else {
+                place.o[r][d] = o;
+                if (d == 0) place.m[r] = m, place.l[r] = l;
+            }
+        }
+        __syncthreads();
+        at += r1 - r0;
+    }
+}
+
+// The heads that several of the n CTAs share, and zeros for idle rows: one
+// block per row, its groups of D threads taking parts in turn.
+template <int ROWS, int D, int kJoinThreads>
+__global__ void __launch_bounds__(kJoinThreads) swa_step_join_kernel(SwaStepArgs p, const Part<ROWS, D>* places, int ctas) {
+    using bf = __nv_bfloat16;
+    constexpr int kGroups = kJoinThreads / D;
+    __shared__ float weight[kStreamCtas], sum[kGroups][D], red[2][32];
+    const int G = p.Hq / p.Hkv, hgroups = (G + ROWS - 1) / ROWS, heads = p.Hkv * hgroups, cap = p.sinks + p.window;
+    const int tid = threadIdx.x, b = blockIdx.y, hk = blockIdx.x / G, qh = blockIdx.x % G, r = qh % ROWS;
+    const int head = hk * hgroups + qh / ROWS, runs = runs_of(p.pos[b], cap);
+    bf* out = static_cast<bf*>(p.out) + ((size_t)b * p.Hq + blockIdx.x) * D;
+    long long before, total;
+    count_runs(p.pos, p.B, b, cap, before, total);
+    if (runs == 0) {
+        cudaGridDependencySynchronize();
+        if (tid < D) out[tid] = to_out<bf>(0.f);
+        return;
+    }
+    total *= heads;
+    const long long n = shares(ctas, total);
+    const long long s = before * heads + (long long)head * runs, e = s + runs;
+    const long long i0 = ((s + 1) * n - 1) / total, i1 = (e * n - 1) / total;       // the CTAs of its first and last run
+    cudaGridDependencySynchronize();                        // the parts are complete
+    if (i0 == i1) return;
+    const int lead = s == total * i0 / n ? 0 : 1;           // place of the first CTA's part
+    const int count = (int)(i1 - i0 + 1);                   // <= ctas = kStreamCtas
+    auto part = [&](int w) -> const Part<ROWS, D>& { return places[2 * (i0 + w) + (w == 0 ? lead : 0)]; };
+    // every thread holds the maximum and sum of up to kMine parts
+    constexpr int kMine = (kStreamCtas + kJoinThreads - 1) / kJoinThreads;
+    float pm[kMine], pl[kMine], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int w = tid + i * kJoinThreads;
+        pm[i] = w < count ? part(w).m[r] : -INFINITY;
+        pl[i] = w < count ? part(w).l[r] : 0.f;
+        m = fmaxf(m, pm[i]);
+    }
+#pragma unroll
+    for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, k));
+    if ((tid & 31) == 0) red[0][tid >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[0][w]);           // finite: every run has a slot
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int w = tid + i * kJoinThreads;
+        const float f = exp2f(pm[i] - m);
+        if (w < count) weight[w] = f;
+        l = fmaf(pl[i], f, l);
+    }
+#pragma unroll
+    for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(~0u, l, k);
+    if ((tid & 31) == 0) red[1][tid >> 5] = l;
+    __syncthreads();
+    float o = 0.f;
+#pragma unroll 16
+    for (int w = tid / D; w < count; w += kGroups) o = fmaf(part(w).o[r][tid % D], weight[w], o);
+    sum[tid / D][tid % D] = o;
+    __syncthreads();
+    if (tid >= D) return;
+    l = 0.f, o = 0.f;
+    for (int w = 0; w < kJoinThreads / 32; ++w) l += red[1][w];
+#pragma unroll
+    for (int w = 0; w < kGroups; ++w) o += sum[w][tid];
+    out[tid] = to_out<bf>(o / l);
 }
 
 // ---- rolling cache of a prompt ----
@@ -386,20 +596,22 @@ __global__ void swa_cache_fill_kernel(const uint4* __restrict__ k, const uint4* 
     }
 }
 
+// CTAs per head and sequence, in a cluster: doubled while the grid is below
+// three CTAs per SM and every CTA's warps still get a run of slots
+int splits_for(long long blocks, int slots_per_round, long long slots) {
+    int n = 1;
+    while (n < kMaxSplits && blocks * n < 3 * 148 && 2LL * n * slots_per_round <= slots) n *= 2;
+    return n;
+}
+
 template <typename F>
-cudaError_t launch_step(F* kernel, const SwaStepArgs& a, int rows_per_cta, int slots_per_round, int threads,
-                        int smem, cudaStream_t st) {
-    const int G = a.Hq / a.Hkv, hgroups = (G + rows_per_cta - 1) / rows_per_cta;
-    const long long blocks = (long long)a.B * a.Hkv * hgroups;
-    // CTAs per head and sequence: doubled while the grid is below three CTAs
-    // per SM and every CTA's warps still get a run of slots
-    int splits = 1;
-    while (splits < kMaxSplits && blocks * splits < 3 * 148 &&
-           (long long)2 * splits * slots_per_round <= (long long)a.sinks + a.window)
-        splits *= 2;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess && splits > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
+cudaError_t launch_cluster(F* kernel, const SwaStepArgs& a, int hgroups, int slots_per_round, int threads, int smem,
+                           cudaStream_t st) {
+    const int splits = splits_for((long long)a.B * a.Hkv * hgroups, slots_per_round, (long long)a.sinks + a.window);
+    if (splits > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(splits, a.Hkv * hgroups, a.B);
     cfg.blockDim = dim3(threads);
@@ -414,23 +626,63 @@ cudaError_t launch_step(F* kernel, const SwaStepArgs& a, int rows_per_cta, int s
     return cudaLaunchKernelEx(&cfg, kernel, a, splits);
 }
 
+// The second launch costs about 2 us: worth it from some MB of cache on.
+bool use_stream(const SwaStepArgs& a) {
+    if (a.dtype != MESA_BF16 || (a.d != 64 && a.d != 128)) return false;
+    return (long long)a.B * a.Hkv * ((long long)a.sinks + a.window) * a.d * 4 >= (8LL << 20);
+}
+
 template <int ROWS, int D>
 cudaError_t step_mma(const SwaStepArgs& a, cudaStream_t st) {
-    return launch_step(swa_step_mma_kernel<ROWS, D>, a, ROWS, kMmaWarps * 16, kMmaThreads,
-                       (int)sizeof(Part<ROWS, D>) * kMmaWarps, st);
+    const int hgroups = (a.Hq / a.Hkv + ROWS - 1) / ROWS;
+    if (!use_stream(a)) {
+        constexpr int smem = (int)sizeof(Part<ROWS, D>) * (kMmaWarps + 1);
+        static_assert(smem <= 48 * 1024, "no opt-in needed");
+        return launch_cluster(swa_step_cluster_kernel<ROWS, D>, a, hgroups, kRound, kMmaThreads, smem, st);
+    }
+    Part<ROWS, D>* places = static_cast<Part<ROWS, D>*>(a.workspace);
+    swa_step_stream_kernel<ROWS, D><<<kStreamCtas, kMmaThreads, sizeof(Part<ROWS, D>) * kMmaWarps, st>>>(a, places);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // about this many parts a head: a block's threads share long lists of them
+    const bool many = kStreamCtas / ((long long)a.B * a.Hkv * hgroups) >= 16;
+    const int threads = many ? 1024 : 128;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.Hq, a.B);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, many ? swa_step_join_kernel<ROWS, D, 1024> : swa_step_join_kernel<ROWS, D, 128>, a,
+                              static_cast<const Part<ROWS, D>*>(places), kStreamCtas);
+}
+
+template <typename T, int D>
+cudaError_t step_simt_d(const SwaStepArgs& a, cudaStream_t st) {
+    return launch_cluster(swa_step_simt_kernel<T, D>, a, (a.Hq / a.Hkv + kSimtRows - 1) / kSimtRows, kSimtThreads,
+                          kSimtThreads, 0, st);
 }
 
 template <typename T>
 cudaError_t step_simt(const SwaStepArgs& a, cudaStream_t st) {
     switch (a.d) {
-        case 16: return launch_step(swa_step_simt_kernel<T, 16>, a, kSimtRows, kSimtThreads, kSimtThreads, 0, st);
-        case 32: return launch_step(swa_step_simt_kernel<T, 32>, a, kSimtRows, kSimtThreads, kSimtThreads, 0, st);
-        case 64: return launch_step(swa_step_simt_kernel<T, 64>, a, kSimtRows, kSimtThreads, kSimtThreads, 0, st);
-        default: return launch_step(swa_step_simt_kernel<T, 128>, a, kSimtRows, kSimtThreads, kSimtThreads, 0, st);
+        case 16: return step_simt_d<T, 16>(a, st);
+        case 32: return step_simt_d<T, 32>(a, st);
+        case 64: return step_simt_d<T, 64>(a, st);
+        default: return step_simt_d<T, 128>(a, st);
     }
 }
 
 }  // namespace
+
+size_t swa_step_workspace_bytes(const SwaStepArgs& a) {
+    if (!use_stream(a)) return 0;
+    const size_t row = (size_t)(a.d + 2) * sizeof(float);
+    return 2 * kStreamCtas * (a.Hq / a.Hkv > 8 ? 16 : 8) * row;
+}
 
 cudaError_t swa_step(const SwaStepArgs& a, cudaStream_t st) {
     LaunchTimer lt(kKindSwaStep, st);

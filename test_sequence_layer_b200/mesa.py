@@ -98,7 +98,9 @@ def _load():
     lib.mesa_swa_backward_workspace_size.restype = Z
     lib.mesa_swa_backward.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, I, P, P, P, P, Z, P]
     lib.mesa_swa_backward.restype = I
-    lib.mesa_swa_step.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, F, I, P, P]
+    lib.mesa_swa_step_workspace_size.argtypes = [I, I, I, I, I, I, I]
+    lib.mesa_swa_step_workspace_size.restype = Z
+    lib.mesa_swa_step.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, F, I, P, P, Z, P]
     lib.mesa_swa_step.restype = I
     lib.mesa_swa_cache_fill.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, P]
     lib.mesa_swa_cache_fill.restype = I
@@ -432,65 +434,86 @@ def forward_noalloc(q, k, v, gamma, beta, lam, *, chunk=64, cg_steps=15, tol=0.0
 
 # ---- the other mixers of a hybrid stack (include/mesa_mixers.h) ----
 
-def _arg(name, t, shape, dtype, device):
-    """A CUDA tensor the library may take by its pointer: shape, type, device, contiguous."""
+def _arg(name, t, shape, dtype, index):
+    """Checks that the library may take t by its pointer: shape, type, CUDA device, contiguous."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return
+    except (AttributeError, RuntimeError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    if t.device.type != "cuda" or t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{max(index, 0)}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _first(name, t, dims):
-    """The argument that fixes type, sizes and device of a call."""
+    """Device index of the argument that fixes type, sizes and device of a call."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
-    if t.dtype not in (torch.float32, torch.bfloat16):
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    return _arg(name, t, t.shape, t.dtype, t.device)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.get_device()
 
 
 class _On:
-    """Runs a call on the tensors' device; what it allocates belongs to its stream."""
+    """Runs a call on the tensors' device; what it allocates belongs to its
+    stream. `raw` is that stream's handle."""
 
-    def __init__(self, device, stream):
-        self.device = torch.cuda.device(device)
-        self.stream = None if stream is None else torch.cuda.stream(stream)
+    __slots__ = ("contexts", "raw")
+
+    def __init__(self, index, stream):
+        self.contexts = ()
+        if torch.cuda.current_device() != index:
+            self.contexts = (torch.cuda.device(index),)
+        if stream is None:
+            self.raw = torch._C._cuda_getCurrentRawStream(index)
+        else:
+            self.contexts += (torch.cuda.stream(stream),)
+            self.raw = stream.cuda_stream
 
     def __enter__(self):
-        self.device.__enter__()
-        if self.stream is not None:
-            self.stream.__enter__()
+        for c in self.contexts:
+            c.__enter__()
+        return self.raw
 
     def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        self.device.__exit__(*exc)
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
 
 
-def _workspace(given, need, device):
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _workspace(given, need, device, index):
     if given is None:
         return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-    if not given.is_cuda or given.device != device or not given.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
+    if given.get_device() != index or not given.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{index}")
     return given
 
 
 def _lru_inputs(x, gate_a, gate_x, lam, dims):
-    _first("x", x, dims)
-    if x.shape[0] < 1 or x.shape[-1] < 1:
-        raise ValueError(f"x needs at least one sequence and one channel, got {tuple(x.shape)}")
-    _arg("gate_a", gate_a, x.shape, x.dtype, x.device)
-    _arg("gate_x", gate_x, x.shape, x.dtype, x.device)
-    _arg("lam", lam, x.shape[-1:], torch.float32, x.device)
+    index = _first("x", x, dims)
+    shape, dtype = x.shape, x.dtype
+    if shape[0] < 1 or shape[-1] < 1:
+        raise ValueError(f"x needs at least one sequence and one channel, got {tuple(shape)}")
+    _arg("gate_a", gate_a, shape, dtype, index)
+    _arg("gate_x", gate_x, shape, dtype, index)
+    _arg("lam", lam, shape[-1:], torch.float32, index)
+    return index
 
 
 def lru_forward(x, gate_a, gate_x, lam, *, h0=None, y=None, return_state=False, return_saved=False, stream=None):
@@ -504,18 +527,18 @@ def lru_forward(x, gate_a, gate_x, lam, *, h0=None, y=None, return_state=False, 
     takes ([B, ceil(T/64), D] float32) if return_saved.
     """
     lib = _load()
-    _lru_inputs(x, gate_a, gate_x, lam, 3)
+    index = _lru_inputs(x, gate_a, gate_x, lam, 3)
     (B, T, D), dev = x.shape, x.device
     if h0 is not None:
-        _arg("h0", h0, (B, D), torch.float32, dev)
+        _arg("h0", h0, (B, D), torch.float32, index)
     if y is not None:
-        _arg("y", y, x.shape, x.dtype, dev)
-    with _On(dev, stream):
+        _arg("y", y, x.shape, x.dtype, index)
+    with _On(index, stream) as raw:
         y = torch.empty_like(x) if y is None else y
         h_T = torch.empty((B, D), dtype=torch.float32, device=dev) if return_state else None
         saved = torch.empty((B, -(-T // 64), D), dtype=torch.float32, device=dev) if return_saved else None
-        _check(lib.mesa_lru_forward(_ptr(x), _ptr(gate_a), _ptr(gate_x), _ptr(lam), B, T, D, _dtype_code(x), _ptr(h0),
-                                    _ptr(y), _ptr(h_T), _ptr(saved), _stream(stream, dev)), "mesa_lru_forward")
+        _check(lib.mesa_lru_forward(_p(x), _p(gate_a), _p(gate_x), _p(lam), B, T, D, _dtype_code(x), _p(h0),
+                                    _p(y), _p(h_T), _p(saved), raw), "mesa_lru_forward")
     res = (y,) + ((h_T,) if return_state else ()) + ((saved,) if return_saved else ())
     return res[0] if len(res) == 1 else res
 
@@ -527,25 +550,25 @@ def lru_backward(x, gate_a, gate_x, lam, dy, *, h0=None, saved=None, dh_T=None, 
     Returns (dx, dgate_a, dgate_x, dlam, dh0): the first three in x's type,
     dlam [D] and dh0 [B,D] float32."""
     lib = _load()
-    _lru_inputs(x, gate_a, gate_x, lam, 3)
+    index = _lru_inputs(x, gate_a, gate_x, lam, 3)
     (B, T, D), dev, code = x.shape, x.device, _dtype_code(x)
-    _arg("dy", dy, x.shape, x.dtype, dev)
+    _arg("dy", dy, x.shape, x.dtype, index)
     if h0 is not None:
-        _arg("h0", h0, (B, D), torch.float32, dev)
+        _arg("h0", h0, (B, D), torch.float32, index)
     if saved is not None:
-        _arg("saved", saved, (B, -(-T // 64), D), torch.float32, dev)
+        _arg("saved", saved, (B, -(-T // 64), D), torch.float32, index)
     if dh_T is not None:
-        _arg("dh_T", dh_T, (B, D), torch.float32, dev)
-    with _On(dev, stream):
+        _arg("dh_T", dh_T, (B, D), torch.float32, index)
+    with _On(index, stream) as raw:
         dx, dga, dgx = (torch.empty_like(x) for _ in range(3))
         dlam = torch.empty(D, dtype=torch.float32, device=dev)
         dh0 = torch.empty((B, D), dtype=torch.float32, device=dev)
         need = int(lib.mesa_lru_backward_workspace_size(B, T, D, code, saved is not None))
-        workspace = _workspace(workspace, need, dev)
-        _check(lib.mesa_lru_backward(_ptr(x), _ptr(gate_a), _ptr(gate_x), _ptr(lam), B, T, D, code, _ptr(h0),
-                                     _ptr(saved), _ptr(dy), _ptr(dh_T), _ptr(dx), _ptr(dga), _ptr(dgx), _ptr(dlam),
-                                     _ptr(dh0), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                     _stream(stream, dev)), "mesa_lru_backward")
+        workspace = _workspace(workspace, need, dev, index)
+        _check(lib.mesa_lru_backward(_p(x), _p(gate_a), _p(gate_x), _p(lam), B, T, D, code, _p(h0),
+                                     _p(saved), _p(dy), _p(dh_T), _p(dx), _p(dga), _p(dgx), _p(dlam),
+                                     _p(dh0), _p(workspace), workspace.numel() * workspace.element_size(),
+                                     raw), "mesa_lru_backward")
     return dx, dga, dgx, dlam, dh0
 
 
@@ -554,29 +577,30 @@ def lru_step(x, gate_a, gate_x, lam, h, *, h_out=None, y=None, stream=None):
     [B,D]; the state h [B,D] float32 is updated in place, or left as it is and
     the new one written to h_out. Returns y [B,D] in x's type."""
     lib = _load()
-    _lru_inputs(x, gate_a, gate_x, lam, 2)
+    index = _lru_inputs(x, gate_a, gate_x, lam, 2)
     (B, D), dev = x.shape, x.device
-    _arg("h", h, (B, D), torch.float32, dev)
+    _arg("h", h, (B, D), torch.float32, index)
     if h_out is not None:
-        _arg("h_out", h_out, (B, D), torch.float32, dev)
+        _arg("h_out", h_out, (B, D), torch.float32, index)
     if y is not None:
-        _arg("y", y, x.shape, x.dtype, dev)
-    with _On(dev, stream):
+        _arg("y", y, x.shape, x.dtype, index)
+    with _On(index, stream) as raw:
         y = torch.empty_like(x) if y is None else y
-        _check(lib.mesa_lru_step(_ptr(x), _ptr(gate_a), _ptr(gate_x), _ptr(lam), B, D, _dtype_code(x), _ptr(h),
-                                 _ptr(h if h_out is None else h_out), _ptr(y), _stream(stream, dev)), "mesa_lru_step")
+        _check(lib.mesa_lru_step(_p(x), _p(gate_a), _p(gate_x), _p(lam), B, D, _dtype_code(x), _p(h),
+                                 _p(h if h_out is None else h_out), _p(y), raw), "mesa_lru_step")
     return y
 
 
 def _swa_inputs(q, k, v, dims):
     """Checks q [B,Hq,(T,)d] against k, v [B,Hkv,(S,)d]."""
-    _first("q", q, dims)
+    index = _first("q", q, dims)
     if not isinstance(k, torch.Tensor) or k.dim() != dims:
         raise ValueError(f"k must be a tensor of {dims} dimensions")
     if k.shape[0] != q.shape[0] or k.shape[-1] != q.shape[-1]:
         raise ValueError(f"k {tuple(k.shape)} does not go with q {tuple(q.shape)}")
-    _arg("k", k, k.shape, q.dtype, q.device)
-    _arg("v", v, k.shape, q.dtype, q.device)
+    _arg("k", k, k.shape, q.dtype, index)
+    _arg("v", v, k.shape, q.dtype, index)
+    return index
 
 
 def _size(name, v):
@@ -601,15 +625,15 @@ def swa_forward(q, k, v, *, window, sinks=0, scale=None, out=None, return_lse=Fa
     type, plus lse [B,Hq,T] float32 if return_lse.
     """
     lib = _load()
-    _swa_inputs(q, k, v, 4)
+    index = _swa_inputs(q, k, v, 4)
     (B, Hq, T, d), (_, Hkv, S, _), dev = q.shape, k.shape, q.device
     if out is not None:
-        _arg("out", out, q.shape, q.dtype, dev)
-    with _On(dev, stream):
+        _arg("out", out, q.shape, q.dtype, index)
+    with _On(index, stream) as raw:
         out = torch.empty_like(q) if out is None else out
         lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev) if return_lse else None
-        _check(lib.mesa_swa_forward(_ptr(q), _ptr(k), _ptr(v), B, Hq, Hkv, T, S, d, _size("window", window), _size("sinks", sinks),
-                                    _scale(scale, d), _dtype_code(q), _ptr(out), _ptr(lse), _stream(stream, dev)),
+        _check(lib.mesa_swa_forward(_p(q), _p(k), _p(v), B, Hq, Hkv, T, S, d, _size("window", window), _size("sinks", sinks),
+                                    _scale(scale, d), _dtype_code(q), _p(out), _p(lse), raw),
                "mesa_swa_forward")
     return (out, lse) if return_lse else out
 
@@ -618,44 +642,49 @@ def swa_backward(q, k, v, out, lse, dout, *, window, sinks=0, scale=None, worksp
     """Gradients (dq, dk, dv), in the inputs' type, of swa_forward for the
     same arguments, from its out and lse and dout = dL/dout (mesa_swa_backward)."""
     lib = _load()
-    _swa_inputs(q, k, v, 4)
+    index = _swa_inputs(q, k, v, 4)
     (B, Hq, T, d), (_, Hkv, S, _), dev, code = q.shape, k.shape, q.device, _dtype_code(q)
-    _arg("out", out, q.shape, q.dtype, dev)
-    _arg("lse", lse, (B, Hq, T), torch.float32, dev)
-    _arg("dout", dout, q.shape, q.dtype, dev)
-    with _On(dev, stream):
+    _arg("out", out, q.shape, q.dtype, index)
+    _arg("lse", lse, (B, Hq, T), torch.float32, index)
+    _arg("dout", dout, q.shape, q.dtype, index)
+    with _On(index, stream) as raw:
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         need = int(lib.mesa_swa_backward_workspace_size(B, Hq, Hkv, T, S, d, _size("sinks", sinks), code))
-        workspace = _workspace(workspace, need, dev)
-        _check(lib.mesa_swa_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), B, Hq, Hkv, T, S, d,
-                                     _size("window", window), _size("sinks", sinks), _scale(scale, d), code, _ptr(dq), _ptr(dk), _ptr(dv),
-                                     _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                     _stream(stream, dev)), "mesa_swa_backward")
+        workspace = _workspace(workspace, need, dev, index)
+        _check(lib.mesa_swa_backward(_p(q), _p(k), _p(v), _p(out), _p(lse), _p(dout), B, Hq, Hkv, T, S, d,
+                                     _size("window", window), _size("sinks", sinks), _scale(scale, d), code, _p(dq), _p(dk), _p(dv),
+                                     _p(workspace), workspace.numel() * workspace.element_size(),
+                                     raw), "mesa_swa_backward")
     return dq, dk, dv
 
 
-def _caches(k_cache, v_cache, B, Hkv, slots, d, dtype, device):
-    _arg("k_cache", k_cache, (B, Hkv, slots, d), dtype, device)
-    _arg("v_cache", v_cache, (B, Hkv, slots, d), dtype, device)
+def _caches(k_cache, v_cache, B, Hkv, slots, d, dtype, index):
+    _arg("k_cache", k_cache, (B, Hkv, slots, d), dtype, index)
+    _arg("v_cache", v_cache, (B, Hkv, slots, d), dtype, index)
 
 
-def swa_step(q, k, v, k_cache, v_cache, pos, *, window, sinks=0, scale=None, out=None, stream=None):
+def swa_step(q, k, v, k_cache, v_cache, pos, *, window, sinks=0, scale=None, out=None, workspace=None, stream=None):
     """One decoded token over rolling caches (mesa_swa_step): q [B,Hq,d],
     k, v [B,Hkv,d], k_cache, v_cache [B,Hkv,sinks+window,d] updated in place,
     pos [B] int32 on the device: the token's position, negative for an idle
     row (its caches untouched, its output zero). Returns out [B,Hq,d]."""
     lib = _load()
-    _swa_inputs(q, k, v, 3)
-    (B, Hq, d), Hkv, dev = q.shape, k.shape[1], q.device
-    _caches(k_cache, v_cache, B, Hkv, _size("sinks", sinks) + _size("window", window), d, q.dtype, dev)
-    _arg("pos", pos, (B,), torch.int32, dev)
+    index = _swa_inputs(q, k, v, 3)
+    (B, Hq, d), Hkv, dev, code = q.shape, k.shape[1], q.device, _dtype_code(q)
+    window, sinks = _size("window", window), _size("sinks", sinks)
+    _caches(k_cache, v_cache, B, Hkv, sinks + window, d, q.dtype, index)
+    _arg("pos", pos, (B,), torch.int32, index)
     if out is not None:
-        _arg("out", out, q.shape, q.dtype, dev)
-    with _On(dev, stream):
+        _arg("out", out, q.shape, q.dtype, index)
+    with _On(index, stream) as raw:
         out = torch.empty_like(q) if out is None else out
-        _check(lib.mesa_swa_step(_ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(pos), B, Hq, Hkv, d,
-                                 _size("window", window), _size("sinks", sinks), _scale(scale, d), _dtype_code(q), _ptr(out),
-                                 _stream(stream, dev)), "mesa_swa_step")
+        need = lib.mesa_swa_step_workspace_size(B, Hq, Hkv, d, window, sinks, code)
+        if need or workspace is not None:
+            workspace = _workspace(workspace, need, dev, index)
+        _check(lib.mesa_swa_step(_p(q), _p(k), _p(v), _p(k_cache), _p(v_cache), _p(pos), B, Hq, Hkv, d, window, sinks,
+                                 _scale(scale, d), code, _p(out), _p(workspace),
+                                 0 if workspace is None else workspace.numel() * workspace.element_size(), raw),
+               "mesa_swa_step")
     return out
 
 
@@ -664,13 +693,13 @@ def swa_cache_fill(k, v, k_cache, v_cache, *, window, sinks=0, start=0, lens=Non
     into rolling caches (mesa_swa_cache_fill), as S swa_step calls would.
     lens: int32 [B] on the device, the tokens of each sequence (None: S)."""
     lib = _load()
-    _first("k", k, 4)
+    index = _first("k", k, 4)
     (B, Hkv, S, d), dev = k.shape, k.device
-    _arg("v", v, k.shape, k.dtype, dev)
-    _caches(k_cache, v_cache, B, Hkv, _size("sinks", sinks) + _size("window", window), d, k.dtype, dev)
+    _arg("v", v, k.shape, k.dtype, index)
+    _caches(k_cache, v_cache, B, Hkv, _size("sinks", sinks) + _size("window", window), d, k.dtype, index)
     if lens is not None:
-        _arg("lens", lens, (B,), torch.int32, dev)
-    with _On(dev, stream):
-        _check(lib.mesa_swa_cache_fill(_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(lens), B, Hkv, S, d,
-                                       _size("window", window), _size("sinks", sinks), _size("start", start), _dtype_code(k), _stream(stream, dev)),
+        _arg("lens", lens, (B,), torch.int32, index)
+    with _On(index, stream) as raw:
+        _check(lib.mesa_swa_cache_fill(_p(k), _p(v), _p(k_cache), _p(v_cache), _p(lens), B, Hkv, S, d,
+                                       _size("window", window), _size("sinks", sinks), _size("start", start), _dtype_code(k), raw),
                "mesa_swa_cache_fill")

@@ -102,7 +102,7 @@ def test_swa_backward_refusals(lib, kw, want):
 
 def swa_step(lib, **kw):
     a = dict(q=A[0], k=A[1], v=A[2], kc=A[3], vc=A[4], pos=A[5], B=2, Hq=4, Hkv=2, d=64, window=8, sinks=2,
-             scale=ctypes.c_float(0.1), dt=1, out=A[6])
+             scale=ctypes.c_float(0.1), dt=1, out=A[6], ws=A[7], n=1 << 24)
     a.update(kw)
     return lib.mesa_swa_step(*a.values(), None)
 
@@ -110,7 +110,9 @@ def swa_step(lib, **kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(pos=None), INVALID), (dict(pos=A[5] + 2), INVALID), (dict(kc=None), INVALID), (dict(vc=A[3]), INVALID),
     (dict(out=A[0]), INVALID), (dict(out=A[3] + 16), INVALID), (dict(Hq=5), INVALID), (dict(window=0), INVALID),
-    (dict(window=2 ** 31 - 1), UNSUPPORTED), (dict(sinks=200), UNSUPPORTED), (dict(d=24), UNSUPPORTED)])
+    (dict(window=2 ** 31 - 1), UNSUPPORTED), (dict(sinks=200), UNSUPPORTED), (dict(d=24), UNSUPPORTED),
+    (dict(window=1 << 20, ws=None), WORKSPACE), (dict(window=1 << 20, n=100), WORKSPACE),
+    (dict(window=1 << 20, ws=A[7] + 16), INVALID), (dict(window=1 << 20, ws=A[6]), INVALID)])
 def test_swa_step_refusals(lib, kw, want):
     assert swa_step(lib, **kw) == want
 
