@@ -148,8 +148,8 @@ swa_tc_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         for (int i = 0; i < 2; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 1);
         mbar_init(bar_q, 1);
         mbar_init(s_full, 1);
-        mbar_init(dp_free, 256);
-        mbar_init(ds_ready, 256);
+        mbar_init(dp_free, 8);
+        mbar_init(ds_ready, 8);
         mbar_init(done, 1);
         fence_mbar_init();
     }
@@ -169,12 +169,12 @@ swa_tc_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             }
             for (int n = 0; n < kt.n && ok; ++n) {
                 const int sk = n % 3, sv = n & 1, j0 = kt.tile(n) * kTile;
-                ok = mbar_wait(&k_empty[sk], ((n / 3) & 1) ^ 1);
+                ok = swa::wait_bar(&k_empty[sk], ((n / 3) & 1) ^ 1);
                 if (!ok) break;
                 mbar_arrive_expect_tx(&k_full[sk], L::kBytes);
                 for (int c = 0; c < D / 64; ++c)
                     swa::tma_load(smem + L::oK + sk * L::kBytes + c * 16384, &mk, c * 64, j0, hkv, &k_full[sk]);
-                ok = mbar_wait(&v_empty[sv], ((n >> 1) & 1) ^ 1);
+                ok = swa::wait_bar(&v_empty[sv], ((n >> 1) & 1) ^ 1);
                 if (!ok) break;
                 mbar_arrive_expect_tx(&v_full[sv], L::kBytes);
                 for (int c = 0; c < D / 64; ++c)
@@ -195,27 +195,27 @@ swa_tc_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 }
             };
             auto scores = [&](int n) {
-                if (!mbar_wait(&k_full[n % 3], (n / 3) & 1)) return false;
+                if (!swa::wait_bar(&k_full[n % 3], (n / 3) & 1)) return false;
                 product(tm + 128 * (n & 1), sq, sk + (n % 3) * L::kBytes);
                 return true;
             };
             auto dprobs = [&](int n) {
-                if (!mbar_wait(&v_full[n & 1], (n >> 1) & 1)) return false;
+                if (!swa::wait_bar(&v_full[n & 1], (n >> 1) & 1)) return false;
                 product(tDp, sdo, sv + (n & 1) * L::kBytes);
                 mma_commit(s_full);
                 mma_commit(&v_empty[n & 1]);
                 return true;
             };
-            ok = mbar_wait(bar_q, 0) && scores(0) && dprobs(0);
+            ok = swa::wait_bar(bar_q, 0) && scores(0) && dprobs(0);
             if (ok && kt.n > 1) ok = scores(1);
             for (int n = 0; n < kt.n && ok; ++n) {
                 if (n + 1 < kt.n) {
-                    ok = mbar_wait(dp_free, n & 1);
+                    ok = swa::wait_bar(dp_free, n & 1);
                     tc_fence_after();
                     ok = ok && dprobs(n + 1);
                     if (!ok) break;
                 }
-                ok = mbar_wait(ds_ready, n & 1);
+                ok = swa::wait_bar(ds_ready, n & 1);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t k = sk + (n % 3) * L::kBytes;
@@ -226,7 +226,7 @@ swa_tc_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 if (n + 2 < kt.n) ok = scores(n + 2);
             }
             mma_commit(done);
-            mbar_wait(done, 0);                      // nothing in flight when tensor memory is freed
+            swa::wait_bar(done, 0);                      // nothing in flight when tensor memory is freed
         }
     } else {
         // warps 0-3 take columns 0-63 of a row, warps 4-7 columns 64-127
@@ -236,7 +236,7 @@ swa_tc_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         const float sc = a.scale * swa::kLog2e;
         for (int n = 0; n < kt.n; ++n) {
             const int j0 = kt.tile(n) * kTile;
-            ok = mbar_wait(s_full, n & 1);
+            ok = swa::wait_bar(s_full, n & 1);
             if (!ok) break;
             tc_fence_after();
             const uint32_t tS = tm + 128 * (n & 1) + lanes;
@@ -248,7 +248,8 @@ swa_tc_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             }
             tmem_wait_ld();
             tc_fence_before();
-            swa::mbar_arrive(dp_free);
+            __syncwarp();
+            if (lane == 0) swa::mbar_arrive(dp_free);
             const bool whole = j0 + kTile - 1 <= p0 && p0 + kTile - 1 - j0 < a.window;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -266,9 +267,10 @@ swa_tc_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             }
             tmem_wait_st();
             tc_fence_before();
-            swa::mbar_arrive(ds_ready);
+            __syncwarp();
+            if (lane == 0) swa::mbar_arrive(ds_ready);
         }
-        if (ok) ok = mbar_wait(done, 0);
+        if (ok) ok = swa::wait_bar(done, 0);
         tc_fence_after();
         const int t = t0 + row;
         store_row<D>(static_cast<__nv_bfloat16*>(f.dq) + ((size_t)head * a.T + t) * D, tDq + lanes, half * (D / 2), D / 2,
@@ -326,7 +328,7 @@ swa_tc_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
     if (tid == 0) {
         for (int i = 0; i < L::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         mbar_init(bar_k, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 128);
+        for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 4);
         mbar_init(done, 1);
         fence_mbar_init();
     }
@@ -346,7 +348,7 @@ swa_tc_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
             }
             for (int n = 0; n < steps && ok; ++n) {
                 const int st = n % L::kStages, head = hkv * G + n / per, t = ta + (n % per) * kSub;
-                ok = mbar_wait(&empty[st], ((n / L::kStages) & 1) ^ 1);
+                ok = swa::wait_bar(&empty[st], ((n / L::kStages) & 1) ^ 1);
                 if (!ok) break;
                 mbar_arrive_expect_tx(&full[st], 2 * L::kPiece + kSub * 8);
                 uint8_t* dst = smem + L::oRing + st * 2 * L::kPiece;
@@ -363,7 +365,7 @@ swa_tc_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
             constexpr uint32_t idO = swa::idesc_bf16(128, D, false, true);
             const uint32_t sk = smem_addr(smem + L::oK), sv = smem_addr(smem + L::oV), sr = smem_addr(smem + L::oRing);
             auto scores = [&](int n) {
-                if (!mbar_wait(&full[n % L::kStages], (n / L::kStages) & 1)) return false;
+                if (!swa::wait_bar(&full[n % L::kStages], (n / L::kStages) & 1)) return false;
                 const uint32_t q = sr + (n % L::kStages) * 2 * L::kPiece, o = q + L::kPiece, t = tm + 128 * (n & 1);
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
@@ -378,10 +380,10 @@ swa_tc_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 mma_commit(&s_full[n & 1]);
                 return true;
             };
-            ok = mbar_wait(bar_k, 0) && scores(0);
+            ok = swa::wait_bar(bar_k, 0) && scores(0);
             if (ok && steps > 1) ok = scores(1);
             for (int n = 0; n < steps && ok; ++n) {
-                ok = mbar_wait(&p_ready[n & 1], (n >> 1) & 1);
+                ok = swa::wait_bar(&p_ready[n & 1], (n >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t q = sr + (n % L::kStages) * 2 * L::kPiece, o = q + L::kPiece, t = tm + 128 * (n & 1);
@@ -395,7 +397,7 @@ swa_tc_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 if (n + 2 < steps) ok = scores(n + 2);
             }
             mma_commit(done);
-            mbar_wait(done, 0);
+            swa::wait_bar(done, 0);
         }
     } else {
         const int grp = warp >> 2, row = (warp & 3) * 32 + lane, j = j0 + row;
@@ -403,8 +405,8 @@ swa_tc_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         const float sc = a.scale * swa::kLog2e;
         for (int n = grp; n < steps; n += 2) {
             const int st = n % L::kStages, q0 = off + ta + (n % per) * kSub;
-            ok = mbar_wait(&full[st], (n / L::kStages) & 1);             // the statistics
-            ok = ok && mbar_wait(&s_full[grp], (n >> 1) & 1);
+            ok = swa::wait_bar(&full[st], (n / L::kStages) & 1);             // the statistics
+            ok = ok && swa::wait_bar(&s_full[grp], (n >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
             const uint32_t tS = tm + 128 * grp + lanes;
@@ -424,9 +426,10 @@ swa_tc_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
             }
             tmem_wait_st();
             tc_fence_before();
-            swa::mbar_arrive(&p_ready[grp]);
+            __syncwarp();
+            if (lane == 0) swa::mbar_arrive(&p_ready[grp]);
         }
-        if (ok && steps > 0) ok = mbar_wait(done, 0);
+        if (ok && steps > 0) ok = swa::wait_bar(done, 0);
         tc_fence_after();
         // warps 0-3 write dv, warps 4-7 dk
         const uint32_t src = (grp ? tDk : tDv) + lanes;

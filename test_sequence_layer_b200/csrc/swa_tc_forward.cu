@@ -2,18 +2,24 @@
 // (bf16, d = 64 or 128).
 //
 // A CTA owns two tiles of 128 queries and walks the 128-key tiles that either
-// may see: the sink tile, then the window. The pair is two heads that share
-// keys where the group allows it, else two consecutive tiles of one head, so
-// that every key tile fetched serves two products. One warp issues the tile
-// copies, one the products, and four warps per query tile do the softmax, one
-// thread per row. Tensor memory holds S0, S1, O0, O1 (128 columns each); P
-// replaces the front half of its S as the bf16 left operand of P V.
+// may see: the sinks, then the window. The pair is two heads that share keys
+// where the group allows it, else two consecutive tiles of one head, so that
+// every key tile fetched serves two products. One warp issues the tile copies,
+// one the products, and eight warps per query tile do the softmax, two threads
+// per row. Tensor memory holds S0, S1, O0, O1 (128 columns each); P replaces
+// the front half of its S as the bf16 left operand of P V.
 //
 // The products are issued in the order PV0(n) S0(n+1) PV1(n) S1(n+1): while
-// one tile's softmax runs, the tensor pipe works for the other.
-// The running maximum m of a row is only a reference for the exponents. It
-// moves when a score passes it by more than 8 (log2 units), and only then are
-// O and l rescaled: P stays below 2^8, which costs bf16 and fp32 nothing.
+// one tile's softmax runs, the tensor pipe works for the other. What bounds the
+// kernel is the chain S -> softmax -> P V -> S of a tile, so the softmax is made
+// short: the running maximum m of a row is only a reference for the exponents.
+// Every thread starts its exponentials on the reference it has while it looks
+// for the tile's maximum; one barrier with a vote both frees the scores for
+// overwriting and tells whether any row passed its reference by more than 8
+// (log2 units). Only then does the reference move and are O and l rescaled: P
+// stays below 2^8, which costs bf16 and fp32 nothing.
+// (64-key tiles with two score buffers take the chain apart, but a product of
+// 128 x 64 x 16 takes the tensor pipe as long as one of 128 x 128 x 16.)
 // P is rounded to bf16 for its product with v; the sum l adds it unrounded.
 #include "swa_tc.cuh"
 
@@ -54,16 +60,24 @@ bool make_map(CUtensorMap* m, const void* base, int d, int rows, int heads, int 
 namespace {
 
 constexpr int kQ = 128, kK = 128;                    // rows of a query and of a key tile
-constexpr int kSoftmaxThreads = 256;
-constexpr int kFwdThreads = kSoftmaxThreads + 64;
+constexpr int kSoftmaxWarps = 16;
+#ifndef KPOLY
+#define KPOLY 0
+#endif
+constexpr int kPoly = KPOLY, kPolyOf = 4;            // share of the exponentials by polynomial
+constexpr int kFwdThreads = kSoftmaxWarps * 32 + 64;
 
 template <int D> struct FwdSmem {
-    static constexpr int kTile = 128 * D * 2;        // bytes of one operand tile
+    static constexpr int kTile = kQ * D * 2;         // bytes of a query tile
+    static constexpr int kPiece = kK * D * 2;        // of a key or value tile
+    static constexpr int kBlock = kK * 128;          // of 64 columns of it
     static constexpr int kStages = D == 128 ? 5 : 8;
     static constexpr int oQ = 0;                     // two query tiles
     static constexpr int oRing = 2 * kTile;          // K and V tiles, in turn
-    static constexpr int oBar = oRing + kStages * kTile;
-    static constexpr int bytes = oBar + (2 * kStages + 8) * 8 + 16 + 1024;   // + slack to align the base
+    static constexpr int oRow = oRing + kStages * kPiece;    // [2 tiles][128] floats
+    static constexpr int oBar = oRow + 1024;
+    static constexpr int bytes = oBar + (2 * kStages + 8) * 8 + 16 + 1008;   // + slack to align the base
+    static_assert(bytes <= 227 * 1024, "more than a CTA has");
 };
 
 struct FwdParams {
@@ -103,6 +117,7 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
     uint64_t* p_full = s_full + 2;                   // [2] weights of tile x are
     uint64_t* o_full = p_full + 2;                   // all products done
     uint32_t* slot = reinterpret_cast<uint32_t*>(o_full + 1);
+    float* rows = reinterpret_cast<float*>(smem + L::oRow);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const SwaArgs& a = f.a;
     const QueryTile q0(f, 0), q1(f, 1);
@@ -118,19 +133,19 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         mbar_init(o_full, 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(&s_full[x], 1);
-            mbar_init(&p_full[x], 128);
+            mbar_init(&p_full[x], 8);
         }
         fence_mbar_init();
     }
-    if (warp == 8) tmem_alloc(slot, 512);
+    if (warp == kSoftmaxWarps) tmem_alloc(slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = *slot;
-    const uint32_t tS[2] = {tm, tm + 128}, tO[2] = {tm + 256, tm + 384};
+    // scores of tile x: columns 128 x; O of tile x: 256 + 128 x
     bool ok = true;
 
-    if (warp == 8) {
+    if (warp == kSoftmaxWarps) {
         if (lane == 0) {
             // ---- copies: the query tiles, then K and V of every key tile ----
             mbar_arrive_expect_tx(bar_q, 2 * L::kTile);
@@ -143,60 +158,60 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 const int st = i % L::kStages;
                 ok = mbar_wait(&empty[st], ((i / L::kStages) & 1) ^ 1);
                 if (!ok) break;
-                mbar_arrive_expect_tx(&full[st], L::kTile);
+                mbar_arrive_expect_tx(&full[st], L::kPiece);
                 for (int c = 0; c < D / 64; ++c)
-                    swa::tma_load(smem + L::oRing + st * L::kTile + c * 16384, (i & 1) ? &mv : &mk, c * 64,
+                    swa::tma_load(smem + L::oRing + st * L::kPiece + c * L::kBlock, (i & 1) ? &mv : &mk, c * 64,
                                   kt.tile(i >> 1) * kK, hkv, &full[st]);
             }
         }
-    } else if (warp == 9) {
+    } else if (warp == kSoftmaxWarps + 1) {
         if (lane == 0) {
             // ---- products ----
-            constexpr uint32_t idS = swa::idesc_bf16(128, 128, false, false);
-            constexpr uint32_t idO = swa::idesc_bf16(128, D, false, true);
+            constexpr uint32_t idS = swa::idesc_bf16(kQ, kK, false, false);
+            constexpr uint32_t idO = swa::idesc_bf16(kQ, D, false, true);
             const uint32_t sq = smem_addr(smem + L::oQ), sr = smem_addr(smem + L::oRing);
             uint32_t np[2] = {0, 0};                 // weights taken so far, per tile
-            auto wait_full = [&](int i) { return mbar_wait(&full[i % L::kStages], (i / L::kStages) & 1); };
+            auto wait_full = [&](int i) { return swa::wait_bar(&full[i % L::kStages], (i / L::kStages) & 1); };
             auto scores = [&](int x, int it) {
-                const uint32_t k = sr + (2 * it % L::kStages) * L::kTile, q = sq + x * L::kTile;
+                const uint32_t k = sr + (2 * it % L::kStages) * L::kPiece, q = sq + x * L::kTile;
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
                     const uint32_t o = (s / 4) * 16384 + (s % 4) * 32;
-                    mma_f16(tS[x], sdesc(q + o, 0, 1024), sdesc(k + o, 0, 1024), idS, s > 0);
+                    mma_f16(tm + 128 * x, sdesc(q + o, 0, 1024), sdesc(k + o, 0, 1024), idS, s > 0);
                 }
                 mma_commit(&s_full[x]);
             };
             auto values = [&](int x, int it) {
-                const uint32_t v = sr + ((2 * it + 1) % L::kStages) * L::kTile;
+                const uint32_t v = sr + ((2 * it + 1) % L::kStages) * L::kPiece;
 #pragma unroll
                 for (int s = 0; s < kK / 16; ++s)
-                    swa::mma_ts(tO[x], tS[x] + 8 * s, sdesc(v + s * 2048, 16384, 1024), idO, np[x] > 0 || s > 0);
+                    swa::mma_ts(tm + 256 + 128 * x, tm + 128 * x + 8 * s, sdesc(v + s * 2048, L::kBlock, 1024), idO,
+                                np[x] > 0 || s > 0);
                 ++np[x];
             };
-            ok = mbar_wait(bar_q, 0) && wait_full(0);
+            ok = swa::wait_bar(bar_q, 0) && wait_full(0);
+            bool use[2] = {q0.uses(kt.tile(0) * kK, a.window, a.sinks), q1.uses(kt.tile(0) * kK, a.window, a.sinks)};
             if (ok) {
-                const int j = kt.tile(0) * kK;
-                if (q0.uses(j, a.window, a.sinks)) scores(0, 0);
-                if (q1.uses(j, a.window, a.sinks)) scores(1, 0);
+                if (use[0]) scores(0, 0);
+                if (use[1]) scores(1, 0);
                 mma_commit(&empty[0]);
             }
             for (int it = 0; it < kt.n && ok; ++it) {
-                const int j = kt.tile(it) * kK, jn = kt.tile(it + 1) * kK;
+                const int jn = kt.tile(it + 1) * kK;
                 const bool more = it + 1 < kt.n;
-                ok = wait_full(2 * it + 1);
-                for (int x = 0; x < 2 && ok; ++x) {
-                    const QueryTile& q = x ? q1 : q0;
-                    if (q.uses(j, a.window, a.sinks)) {
-                        ok = mbar_wait(&p_full[x], np[x] & 1);
-                        if (!ok) break;
+                const bool next[2] = {more && q0.uses(jn, a.window, a.sinks), more && q1.uses(jn, a.window, a.sinks)};
+                ok = wait_full(2 * it + 1) && (!more || wait_full(2 * it + 2));
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (use[x] && ok) {
+                        ok = swa::wait_bar(&p_full[x], np[x] & 1);
                         tc_fence_after();
-                        values(x, it);
+                        if (ok) values(x, it);
                     }
                     if (x == 1) mma_commit(&empty[(2 * it + 1) % L::kStages]);
-                    if (!more) continue;
-                    if (x == 0) ok = wait_full(2 * it + 2);
-                    if (ok && q.uses(jn, a.window, a.sinks)) scores(x, it + 1);
-                    if (ok && x == 1) mma_commit(&empty[(2 * it + 2) % L::kStages]);
+                    if (next[x] && ok) scores(x, it + 1);
+                    if (x == 1 && more) mma_commit(&empty[(2 * it + 2) % L::kStages]);
+                    use[x] = next[x];
                 }
             }
             mma_commit(o_full);
@@ -204,100 +219,131 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
             mbar_wait(o_full, 0);
         }
     } else {
-        // ---- softmax of tile x, one row per thread ----
-        const int x = warp >> 2;
-        const QueryTile& q = x ? q1 : q0;
+        // ---- softmax of tile x: columns 64 half .. of a row per thread. A
+        // thread that gave up a wait goes on without waiting, so that the
+        // others' barriers are met. ----
+        const int x = warp >> 3, half = (warp >> 2) & 1;
+        const QueryTile q(f, x);
         const int row = (warp & 3) * 32 + lane, pos = q.p0 + row;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const float sc = a.scale * swa::kLog2e, slack = 8.f / sc;
+        const uint32_t tS = tm + 128 * x + lanes, tO = tm + 256 + 128 * x + half * (D / 2) + lanes;
+        float* shared_row = rows + x * kQ + row;     // between the two threads of a row
+        auto exchange = [&](float v, auto combine) { // half 0 hands its value over and takes the result
+            if (half == 0) *shared_row = v;
+            swa::bar_sync(1 + x, 256);
+            if (half == 1) *shared_row = v = combine(*shared_row, v);
+            swa::bar_sync(1 + x, 256);
+            return half == 0 ? *shared_row : v;
+        };
+        const float sc = a.scale * swa::kLog2e;
+        constexpr float kLimit = 256.f;
+        const float2 sc2 = make_float2(sc, sc);
         float m = -INFINITY;
         float2 l2 = make_float2(0.f, 0.f);
         uint32_t n = 0;
         for (int it = 0; it < kt.n; ++it) {
             const int j0 = kt.tile(it) * kK;
             if (!q.uses(j0, a.window, a.sinks)) continue;
-            ok = mbar_wait(&s_full[x], n & 1);
-            if (!ok) break;
+            if (ok) ok = swa::wait_bar(&s_full[x], n & 1);
             tc_fence_after();
-            float s[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32_x32(tS[x] + lanes + 32 * c, s[c]);
-            tmem_wait_ld();
+            float s[2][32], pk[2][16];
             const bool whole = j0 + kK - 1 <= q.p0 && q.p0 + kQ - 1 - j0 < a.window;
-            if (!whole) {
-                const int hi = pos - j0, lo = pos - a.window + 1 - j0, sk = a.sinks - j0;
+            auto fetch = [&]() {
+                tmem_ld32_x32(tS + 64 * half, s[0]);
+                tmem_ld32_x32(tS + 64 * half + 32, s[1]);
+                tmem_wait_ld();
+                if (whole) return;
+                const int c0 = j0 + 64 * half;
+                const int hi = pos - c0, lo = pos - a.window + 1 - c0, sk = a.sinks - c0;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         const int j = 32 * c + e;
                         if (!(j <= hi && (j >= lo || j < sk))) s[c][e] = -INFINITY;
                     }
-            }
-            float mx[4];
+            };
+            fetch();
+            float2 sum = make_float2(0.f, 0.f);
+            auto weigh = [&](float neg) {
+                const float2 neg2 = make_float2(neg, neg);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                mx[c] = fmaxf(s[c][0], s[c][1]);
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int e = 2; e < 32; e += 2) mx[c] = fmaxf(mx[c], fmaxf(s[c][e], s[c][e + 1]));
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            float keep = 1.f;
-            if (m == -INFINITY) {
-                m = top;                             // O and l hold nothing yet
-            } else if (top > m + slack) {
-                keep = swa::ex2((m - top) * sc);
-                m = top;
-            }
-            if (__any_sync(~0u, keep != 1.f)) {
-                // S(n) is complete, so P V(n - 1), issued before it, is too
-                l2.x *= keep;
-                l2.y *= keep;
+                    for (int e = 0; e < 32; e += 2) {
+                        float2 v = swa::fma2(make_float2(s[c][e], s[c][e + 1]), sc2, neg2);
+                        if (e / 2 % kPolyOf < kPoly) {
+                            v = swa::ex2_poly(v);
+                        } else {
+                            v.x = swa::ex2(v.x);
+                            v.y = swa::ex2(v.y);
+                        }
+                        sum = swa::add2(sum, v);
+                        pk[c][e / 2] = __uint_as_float(swa::pack_bf16(v.x, v.y));
+                    }
+            };
+            weigh(-m * sc);
+            // the tile's threads agree on it, and have all read their scores; a row
+            // moves its reference on its own weights alone
+            const bool passed = !(sum.x + sum.y <= kLimit);
+            if (swa::bar_any(1 + x, 256, passed)) {
+                fetch();                             // the weights took the scores' registers
+                float top = s[0][0];
 #pragma unroll
-                for (int c = 0; c < D; c += 16) {
-                    float o[16];
-                    tmem_ld32_x16(tO[x] + lanes + c, o);
-                    tmem_wait_ld();
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] *= keep;
-                    tmem_st32_x16(tO[x] + lanes + c, o);
+                    for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(s[c][e], s[c][e + 1]));
+                auto larger = [](float u, float v) { return fmaxf(u, v); };
+                const bool move = exchange(passed ? 1.f : 0.f, larger) > 0.f;
+                top = exchange(top, larger);
+                float keep = 1.f;
+                if (m == -INFINITY) {
+                    m = top;                         // O and l hold nothing yet
+                } else if (move && top > m) {
+                    keep = swa::ex2((m - top) * sc);
+                    m = top;
                 }
-            }
-            const float neg = m == -INFINITY ? 0.f : -m * sc;
-            const float2 sc2 = make_float2(sc, sc), neg2 = make_float2(neg, neg);
+                if (__any_sync(~0u, keep != 1.f)) {
+                    // S(n) is complete, so P V(n - 1), issued before it, is too
+                    l2.x *= keep;
+                    l2.y *= keep;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float pk[16];
+                    for (int c = 0; c < D / 2; c += 16) {
+                        float o[16];
+                        tmem_ld32_x16(tO + c, o);
+                        tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    float2 v = swa::fma2(make_float2(s[c][e], s[c][e + 1]), sc2, neg2);
-                    v.x = swa::ex2(v.x);
-                    v.y = swa::ex2(v.y);
-                    l2 = swa::add2(l2, v);
-                    pk[e / 2] = __uint_as_float(swa::pack_bf16(v.x, v.y));
+                        for (int e = 0; e < 16; ++e) o[e] *= keep;
+                        tmem_st32_x16(tO + c, o);
+                    }
                 }
-                tmem_st32_x16(tS[x] + lanes + 16 * c, pk);
+                sum = make_float2(0.f, 0.f);
+                weigh(m == -INFINITY ? 0.f : -m * sc);
             }
+            tmem_st32_x16(tS + 32 * half, pk[0]);
+            tmem_st32_x16(tS + 32 * half + 16, pk[1]);
+            l2 = swa::add2(l2, sum);
             tmem_wait_st();
             tc_fence_before();
-            swa::mbar_arrive(&p_full[x]);
+            __syncwarp();
+            if (lane == 0) swa::mbar_arrive(&p_full[x]);
             ++n;
         }
         // ---- output ----
-        if (ok && q.live) {
-            ok = mbar_wait(o_full, 0);
+        if (q.live) {
+            const float l = exchange(l2.x + l2.y, [](float u, float v) { return u + v; }), inv = 1.f / l;
+            if (ok) ok = mbar_wait(o_full, 0);
             tc_fence_after();
-            const int t = q.t0 + row;
-            const bool in = t < a.T;
-            const float l = l2.x + l2.y, inv = 1.f / l;
-            const size_t r = (size_t)q.head * a.T + t;
+            const int tq = q.t0 + row;
+            const bool in = tq < a.T && ok;
+            const size_t r = (size_t)q.head * a.T + tq;
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
+            for (int c = 0; c < D / 2; c += 32) {
                 float o[32];
-                tmem_ld32_x32(tO[x] + lanes + c, o);
+                tmem_ld32_x32(tO + c, o);
                 tmem_wait_ld();
-                if (in && ok) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + r * D + c);
+                if (in) {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + r * D + half * (D / 2) + c);
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
                         dst[e / 8] = make_uint4(swa::pack_bf16(o[e] * inv, o[e + 1] * inv),
@@ -306,13 +352,13 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                                                 swa::pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
                 }
             }
-            if (in && ok && a.lse) a.lse[r] = fmaf(m, a.scale, logf(l));
+            if (in && half == 0 && a.lse) a.lse[r] = fmaf(m, a.scale, logf(l));
             tc_fence_before();
         }
     }
     if (!ok) record_error(f.err, kErrTimeout);
     __syncthreads();
-    if (warp == 8) tmem_dealloc(tm, 512);
+    if (warp == kSoftmaxWarps) tmem_dealloc(tm, 512);
 }
 
 template <int D>
