@@ -74,8 +74,6 @@ mesa_status step_shape(int B, int Hq, int Hkv, int d, int window, int sinks, flo
     return (long long)sinks + window > 0x7fffffffLL ? MESA_ERR_UNSUPPORTED : MESA_OK;
 }
 
-size_t delta_bytes(int B, int Hq, int T) { return round_up((size_t)B * Hq * T * 4, 256); }
-
 }  // namespace
 
 extern "C" {
@@ -179,7 +177,8 @@ mesa_status mesa_swa_forward(const void* q, const void* k, const void* v, int B,
 
 size_t mesa_swa_backward_workspace_size(int B, int Hq, int Hkv, int T, int S, int d, int sinks, mesa_dtype dtype) {
     if (swa_shape(B, Hq, Hkv, d, 1, sinks, 1.f, dtype) != MESA_OK || swa_lengths(T, S) != MESA_OK) return 0;
-    return swa_tc_supported(d, dtype) ? swa_tc_workspace_bytes(B, Hq, Hkv, T, d, sinks) : delta_bytes(B, Hq, T);
+    return swa_tc_supported(d, dtype) ? swa_tc_workspace_bytes(B, Hq, Hkv, T, d, sinks)
+                                      : round_up(swa_simt_workspace_bytes(B, Hq, Hkv, T, S, d, sinks), 256);
 }
 
 mesa_status mesa_swa_backward(const void* q, const void* k, const void* v, const void* out, const float* lse,

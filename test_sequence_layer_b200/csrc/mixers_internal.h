@@ -64,6 +64,7 @@ struct SwaBackwardArgs {
 bool swa_tc_supported(int d, mesa_dtype dtype);
 cudaError_t swa_forward_tc(const SwaArgs& a, cudaStream_t st);
 cudaError_t swa_forward_simt(const SwaArgs& a, cudaStream_t st);
+size_t swa_simt_workspace_bytes(int B, int Hq, int Hkv, int T, int S, int d, int sinks);
 cudaError_t swa_backward_simt(const SwaBackwardArgs& a, cudaStream_t st);
 // tensor cores (swa_tc_backward.cu)
 size_t swa_tc_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int sinks);

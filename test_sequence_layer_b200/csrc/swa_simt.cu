@@ -28,9 +28,23 @@ __device__ __forceinline__ void st_out(__nv_bfloat16* p, float v) { *p = __float
 // the end become zeros
 template <typename T, int D>
 __device__ __forceinline__ void load_tile(float* s, const T* g, int r0, int rows) {
-    for (int i = threadIdx.x; i < kT * D; i += kThreads) {
-        const int r = i / D, c = i % D;
-        s[r * (D + 4) + c] = r0 + r < rows ? ld_in(g, (size_t)(r0 + r) * D + c) : 0.f;
+    constexpr int kPer = 16 / (int)sizeof(T);             // elements of a 16-byte piece
+#pragma unroll 4
+    for (int i = threadIdx.x; i < kT * D / kPer; i += kThreads) {
+        const int r = i / (D / kPer), c = i % (D / kPer) * kPer;
+        float* d = s + r * (D + 4) + c;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r0 + r < rows) v = *reinterpret_cast<const uint4*>(g + (size_t)(r0 + r) * D + c);
+        if (sizeof(T) == 4) {
+            *reinterpret_cast<uint4*>(d) = v;
+        } else {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 8; e += 4)
+                *reinterpret_cast<float4*>(d + e) =
+                    make_float4(__uint_as_float(w[e / 2] << 16), __uint_as_float(w[e / 2] & 0xffff0000u),
+                                __uint_as_float(w[e / 2 + 1] << 16), __uint_as_float(w[e / 2 + 1] & 0xffff0000u));
+        }
     }
 }
 
@@ -60,21 +74,33 @@ __device__ __forceinline__ void dot_tile(const float* A, const float* B, int ty,
 // (W[k][4 ty + i]); W is a padded score tile
 template <int D, bool TRANS>
 __device__ __forceinline__ void weighted_rows(const float* W, const float* B, int ty, int tx, float (&acc)[4][D / 16]) {
+    if (TRANS) {
 #pragma unroll 4
-    for (int k = 0; k < kT; ++k) {
-        float w[4];
-        if (TRANS) {
+        for (int k = 0; k < kT; ++k) {
             const float4 v = *reinterpret_cast<const float4*>(W + k * kPS + 4 * ty);
-            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-        } else {
+            const float w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = W[(4 * ty + i) * kPS + k];
+            for (int c = 0; c < D / 16; ++c) {
+                const float b = B[k * (D + 4) + tx + 16 * c];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i][c] = fmaf(w[i], b, acc[i][c]);
+            }
         }
+    } else {
+#pragma unroll 2
+        for (int k = 0; k < kT; k += 4) {
+            float w[4][4];
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-            const float b = B[k * (D + 4) + tx + 16 * c];
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4*>(w[i]) = *reinterpret_cast<const float4*>(W + (4 * ty + i) * kPS + k);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i][c] = fmaf(w[i], b, acc[i][c]);
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    const float b = B[(k + u) * (D + 4) + tx + 16 * c];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[i][c] = fmaf(w[i][u], b, acc[i][c]);
+                }
         }
     }
 }
@@ -235,8 +261,18 @@ __global__ void __launch_bounds__(kThreads) swa_dq_kernel(SwaBackwardArgs a, con
     }
 }
 
+// How the queries of a key tile are shared out: the tiles that hold a sink, seen
+// by every later query, in chunks of about a window; where key tiles alone do
+// not fill the GPU, each query head of a group apart. A tile of one part writes
+// its gradients; the others leave fp32 parts, added in order afterwards.
+struct DkvPlan {
+    int sink_tiles, chunks, chunk_len, heads;             // heads: parts of a group (1 or G)
+    __host__ __device__ int parts_of(int tile) const { return (tile < sink_tiles ? chunks : 1) * heads; }
+    __host__ __device__ int items(int tiles) const { return (sink_tiles * chunks + tiles - sink_tiles) * heads; }
+};
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) swa_dkv_kernel(SwaBackwardArgs a, const float* delta) {
+__global__ void __launch_bounds__(kThreads) swa_dkv_kernel(SwaBackwardArgs a, const float* delta, DkvPlan pl, float* parts) {
     const SwaArgs& p = a.f;
     extern __shared__ float4 smem4[];
     float* sK = reinterpret_cast<float*>(smem4);
@@ -249,16 +285,26 @@ __global__ void __launch_bounds__(kThreads) swa_dkv_kernel(SwaBackwardArgs a, co
     float* sDl = sL + kT;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int G = p.Hq / p.Hkv, b = blockIdx.y / p.Hkv, hk = blockIdx.y % p.Hkv;
-    const int j0 = blockIdx.x * kT, off = p.S - p.T;
+    const int item = blockIdx.x / pl.heads, hpart = blockIdx.x % pl.heads;
+    const int sink_items = pl.sink_tiles * pl.chunks;
+    const int tile = item < sink_items ? item / pl.chunks : item - sink_items + pl.sink_tiles;
+    const int chunk = item < sink_items ? item % pl.chunks : 0;
+    const int j0 = tile * kT, off = p.S - p.T;
     const size_t kv = ((size_t)b * p.Hkv + hk) * p.S * D;
     load_tile<T, D>(sK, static_cast<const T*>(p.k) + kv, j0, p.S);
     load_tile<T, D>(sV, static_cast<const T*>(p.v) + kv, j0, p.S);
     int ta, tb;
     swa::query_range(j0, min(j0 + kT, p.S) - 1, p.T, p.S, p.window, p.sinks, ta, tb);
+    ta = ta / kT * kT;
+    if (tile < pl.sink_tiles) {
+        ta = max(ta, chunk * pl.chunk_len);
+        tb = min(tb, (chunk + 1) * pl.chunk_len);
+    }
+    const int g0 = pl.heads > 1 ? hpart : 0, g1 = pl.heads > 1 ? hpart + 1 : G;
     float dk[4][D / 16] = {}, dv[4][D / 16] = {};
-    for (int g = 0; g < G; ++g) {
+    for (int g = g0; g < g1; ++g) {
         const size_t row = ((size_t)b * p.Hq + hk * G + g) * p.T;
-        for (int t0 = ta / kT * kT; t0 < tb; t0 += kT) {
+        for (int t0 = ta; t0 < tb; t0 += kT) {
             __syncthreads();
             load_tile<T, D>(sQ, static_cast<const T*>(p.q) + row * D, t0, p.T);
             load_tile<T, D>(sDo, static_cast<const T*>(a.dout) + row * D, t0, p.T);
@@ -270,6 +316,9 @@ __global__ void __launch_bounds__(kThreads) swa_dkv_kernel(SwaBackwardArgs a, co
             weighted_rows<D, true>(sDs, sQ, ty, tx, dk);
         }
     }
+    const bool whole = pl.parts_of(tile) == 1;
+    // this part's place: [2][64][D]
+    float* part = parts + ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 * kT * D;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int j = j0 + 4 * ty + i;
@@ -278,11 +327,58 @@ __global__ void __launch_bounds__(kThreads) swa_dkv_kernel(SwaBackwardArgs a, co
         T* ov = static_cast<T*>(a.dv) + kv + (size_t)j * D;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
-            st_out(ok + tx + 16 * c, dk[i][c]);
-            st_out(ov + tx + 16 * c, dv[i][c]);
+            const int d = tx + 16 * c;
+            if (whole) {
+                st_out(ok + d, dk[i][c]);
+                st_out(ov + d, dv[i][c]);
+            } else {
+                part[(4 * ty + i) * D + d] = dk[i][c];
+                part[(kT + 4 * ty + i) * D + d] = dv[i][c];
+            }
         }
     }
 }
+
+// one tile's parts, added in order: blocks (tile, sequence and head)
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) swa_dkv_sum_kernel(SwaBackwardArgs a, DkvPlan pl, const float* parts, int items) {
+    const int tile = blockIdx.x, n = pl.parts_of(tile);
+    if (n == 1) return;
+    const int first = (tile < pl.sink_tiles ? tile * pl.chunks : pl.sink_tiles * pl.chunks + tile - pl.sink_tiles) * pl.heads;
+    const float* p = parts + ((size_t)blockIdx.y * items + first) * 2 * kT * D;
+    for (int i = threadIdx.x; i < 2 * kT * D; i += kThreads) {
+        const int which = i / (kT * D), r = i % (kT * D), j = tile * kT + r / D;
+        if (j >= a.f.S) continue;
+        float s = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) s += p[(size_t)k * 2 * kT * D + i];
+        st_out(static_cast<T*>(which ? a.dv : a.dk) + ((size_t)blockIdx.y * a.f.S + j) * D + r % D, s);
+    }
+}
+
+// `window` decides the chunks; with 1 the plan has the most parts
+DkvPlan dkv_plan(int B, int Hq, int Hkv, int T, int S, int window, int sinks) {
+    DkvPlan pl{0, 1, T > 0 ? T : 1, 1};
+    const int tiles = (S + kT - 1) / kT;
+    if ((long long)tiles * B * Hkv < 2 * 148) pl.heads = Hq / Hkv;
+    const int sink_tiles = (sinks + kT - 1) / kT < tiles ? (sinks + kT - 1) / kT : tiles;
+    if (sink_tiles == 0) return pl;
+    constexpr int kMaxChunks = 32;
+    long long len = ((long long)window + kT + kT - 1) / kT * kT;
+    const long long least = (((long long)T + kMaxChunks - 1) / kMaxChunks + kT - 1) / kT * kT;
+    if (len < least) len = least;
+    if (len >= T) return pl;
+    pl.sink_tiles = sink_tiles;
+    pl.chunk_len = (int)len;
+    pl.chunks = (int)((T + len - 1) / len);
+    return pl;
+}
+
+size_t dkv_parts_bytes(const DkvPlan& pl, int B, int Hkv, int S, int d) {
+    if (pl.heads == 1 && pl.sink_tiles == 0) return 0;
+    return (size_t)B * Hkv * pl.items((S + kT - 1) / kT) * 2 * kT * d * 4;
+}
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 template <typename K>
 cudaError_t allow_smem(K* kernel, int bytes) {
@@ -304,8 +400,15 @@ cudaError_t bwd(const SwaBackwardArgs& a, const float* delta, cudaStream_t st) {
     cudaError_t e = allow_smem(swa_dq_kernel<T, D>, sq);
     if (e == cudaSuccess) e = allow_smem(swa_dkv_kernel<T, D>, sk);
     if (e != cudaSuccess) return e;
-    swa_dq_kernel<T, D><<<dim3((a.f.T + kT - 1) / kT, a.f.B * a.f.Hq), kThreads, sq, st>>>(a, delta);
-    swa_dkv_kernel<T, D><<<dim3((a.f.S + kT - 1) / kT, a.f.B * a.f.Hkv), kThreads, sk, st>>>(a, delta);
+    const SwaArgs& f = a.f;
+    const DkvPlan pl = dkv_plan(f.B, f.Hq, f.Hkv, f.T, f.S, f.window, f.sinks);
+    const int tiles = (f.S + kT - 1) / kT, items = pl.items(tiles);
+    float* parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + up256((size_t)f.B * f.Hq * f.T * 4));
+    swa_dkv_kernel<T, D><<<dim3(items, f.B * f.Hkv), kThreads, sk, st>>>(a, delta, pl, parts);
+    if (dkv_parts_bytes(pl, f.B, f.Hkv, f.S, D))
+        swa_dkv_sum_kernel<T, D><<<dim3(pl.heads > 1 ? tiles : pl.sink_tiles, f.B * f.Hkv), kThreads, 0, st>>>(a, pl, parts,
+                                                                                                          items);
+    swa_dq_kernel<T, D><<<dim3((f.T + kT - 1) / kT, f.B * f.Hq), kThreads, sq, st>>>(a, delta);
     return cudaGetLastError();
 }
 
@@ -330,6 +433,10 @@ cudaError_t bwd_d(const SwaBackwardArgs& a, const float* delta, cudaStream_t st)
 }
 
 }  // namespace
+
+size_t swa_simt_workspace_bytes(int B, int Hq, int Hkv, int T, int S, int d, int sinks) {
+    return up256((size_t)B * Hq * T * 4) + dkv_parts_bytes(dkv_plan(B, Hq, Hkv, T, S, 1, sinks), B, Hkv, S, d);
+}
 
 cudaError_t swa_delta(const SwaArgs& a, const void* dout, float* delta, cudaStream_t st) {
     const size_t rows = (size_t)a.B * a.Hq * a.T;

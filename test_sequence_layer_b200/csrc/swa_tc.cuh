@@ -99,26 +99,6 @@ __device__ __forceinline__ void bar_sync(int id, int n) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
-// 2^v for two values without the special-function unit, whose rate bounds a
-// softmax: v = n + f with n the nearest integer (added to 1.5 2^23, it ends up
-// in the low bits), 2^f by a polynomial fitted for the least relative error on
-// [-1/2, 1/2] (8e-8), n added to the exponent. Values below -126 count as -126.
-__device__ __forceinline__ float2 ex2_poly(float2 v) {
-    v.x = fmaxf(v.x, -126.f);
-    v.y = fmaxf(v.y, -126.f);
-    const float2 magic = make_float2(12582912.f, 12582912.f);
-    const float2 t = add2(v, magic);
-    const float2 f = fma2(add2(t, make_float2(-12582912.f, -12582912.f)), make_float2(-1.f, -1.f), v);
-    constexpr float c[5] = {0.69314694405f, 0.24022120237f, 0.05550713465f, 0.00967554096f, 0.00132764690f};
-    float2 p = fma2(f, make_float2(c[4], c[4]), make_float2(c[3], c[3]));
-    p = fma2(p, f, make_float2(c[2], c[2]));
-    p = fma2(p, f, make_float2(c[1], c[1]));
-    p = fma2(p, f, make_float2(c[0], c[0]));
-    p = fma2(p, f, make_float2(1.f, 1.f));
-    return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
-                       __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);

@@ -10,8 +10,10 @@
 // the front half of its S as the bf16 left operand of P V.
 //
 // The products are issued in the order PV0(n) S0(n+1) PV1(n) S1(n+1): while
-// one tile's softmax runs, the tensor pipe works for the other. What bounds the
-// kernel is the chain S -> softmax -> P V -> S of a tile, so the softmax is made
+// one tile's softmax runs, the tensor pipe works for the other. (A warp for each
+// tile's products interleaves them and makes both chains longer: 526 us against
+// 437.) What bounds the kernel is the chain S -> softmax -> P V -> S of a tile
+// and the issue of the products, 80 cycles each; so the softmax is made
 // short: the running maximum m of a row is only a reference for the exponents.
 // Every thread starts its exponentials on the reference it has while it looks
 // for the tile's maximum; one barrier with a vote both frees the scores for
@@ -61,11 +63,7 @@ namespace {
 
 constexpr int kQ = 128, kK = 128;                    // rows of a query and of a key tile
 constexpr int kSoftmaxWarps = 16;
-#ifndef KPOLY
-#define KPOLY 0
-#endif
-constexpr int kPoly = KPOLY, kPolyOf = 4;            // share of the exponentials by polynomial
-constexpr int kFwdThreads = kSoftmaxWarps * 32 + 64;
+constexpr int kFwdThreads = kSoftmaxWarps * 32 + 64;      // and a warp of copies, a warp of products
 
 template <int D> struct FwdSmem {
     static constexpr int kTile = kQ * D * 2;         // bytes of a query tile
@@ -164,54 +162,65 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                                   kt.tile(i >> 1) * kK, hkv, &full[st]);
             }
         }
-    } else if (warp == kSoftmaxWarps + 1) {
+    } else if (warp > kSoftmaxWarps) {
         if (lane == 0) {
             // ---- products ----
             constexpr uint32_t idS = swa::idesc_bf16(kQ, kK, false, false);
             constexpr uint32_t idO = swa::idesc_bf16(kQ, D, false, true);
-            const uint32_t sq = smem_addr(smem + L::oQ), sr = smem_addr(smem + L::oRing);
+            const uint64_t dq = sdesc(smem_addr(smem + L::oQ), 0, 1024);
+            const uint64_t dk = sdesc(smem_addr(smem + L::oRing), 0, 1024);
+            const uint64_t dv = sdesc(smem_addr(smem + L::oRing), L::kBlock, 1024);
             uint32_t np[2] = {0, 0};                 // weights taken so far, per tile
-            auto wait_full = [&](int i) { return swa::wait_bar(&full[i % L::kStages], (i / L::kStages) & 1); };
-            auto scores = [&](int x, int it) {
-                const uint32_t k = sr + (2 * it % L::kStages) * L::kPiece, q = sq + x * L::kTile;
+            int st = 0, ph = 0;                      // ring stage of the next tile to take, its phase
+            auto next_stage = [&]() {
+                if (++st == L::kStages) st = 0, ph ^= 1;
+            };
+            // descriptors count in units of 16 bytes
+            auto scores = [&](int x, int stage) {
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
-                    const uint32_t o = (s / 4) * 16384 + (s % 4) * 32;
-                    mma_f16(tm + 128 * x, sdesc(q + o, 0, 1024), sdesc(k + o, 0, 1024), idS, s > 0);
+                    const uint32_t o = ((s / 4) * 16384 + (s % 4) * 32) >> 4;
+                    mma_f16(tm + 128 * x, dq + (x * L::kTile >> 4) + o, dk + (stage * L::kPiece >> 4) + o, idS, s > 0);
                 }
                 mma_commit(&s_full[x]);
             };
-            auto values = [&](int x, int it) {
-                const uint32_t v = sr + ((2 * it + 1) % L::kStages) * L::kPiece;
+            auto values = [&](int x, int stage) {
 #pragma unroll
                 for (int s = 0; s < kK / 16; ++s)
-                    swa::mma_ts(tm + 256 + 128 * x, tm + 128 * x + 8 * s, sdesc(v + s * 2048, L::kBlock, 1024), idO,
+                    swa::mma_ts(tm + 256 + 128 * x, tm + 128 * x + 8 * s, dv + ((stage * L::kPiece + s * 2048) >> 4), idO,
                                 np[x] > 0 || s > 0);
                 ++np[x];
             };
-            ok = swa::wait_bar(bar_q, 0) && wait_full(0);
+            ok = swa::wait_bar(bar_q, 0) && swa::wait_bar(&full[0], 0);
             bool use[2] = {q0.uses(kt.tile(0) * kK, a.window, a.sinks), q1.uses(kt.tile(0) * kK, a.window, a.sinks)};
             if (ok) {
                 if (use[0]) scores(0, 0);
                 if (use[1]) scores(1, 0);
                 mma_commit(&empty[0]);
             }
+            next_stage();
             for (int it = 0; it < kt.n && ok; ++it) {
-                const int jn = kt.tile(it + 1) * kK;
                 const bool more = it + 1 < kt.n;
+                const int jn = kt.tile(it + 1) * kK;
                 const bool next[2] = {more && q0.uses(jn, a.window, a.sinks), more && q1.uses(jn, a.window, a.sinks)};
-                ok = wait_full(2 * it + 1) && (!more || wait_full(2 * it + 2));
+                const int sv = st;
+                ok = swa::wait_bar(&full[st], ph);
+                next_stage();
+                if (more) ok = ok && swa::wait_bar(&full[st], ph);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (use[x] && ok) {
                         ok = swa::wait_bar(&p_full[x], np[x] & 1);
                         tc_fence_after();
-                        if (ok) values(x, it);
+                        if (ok) values(x, sv);
                     }
-                    if (x == 1) mma_commit(&empty[(2 * it + 1) % L::kStages]);
-                    if (next[x] && ok) scores(x, it + 1);
-                    if (x == 1 && more) mma_commit(&empty[(2 * it + 2) % L::kStages]);
+                    if (x == 1) mma_commit(&empty[sv]);
+                    if (next[x] && ok) scores(x, st);
                     use[x] = next[x];
+                }
+                if (more) {
+                    mma_commit(&empty[st]);
+                    next_stage();
                 }
             }
             mma_commit(o_full);
@@ -272,12 +281,8 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         float2 v = swa::fma2(make_float2(s[c][e], s[c][e + 1]), sc2, neg2);
-                        if (e / 2 % kPolyOf < kPoly) {
-                            v = swa::ex2_poly(v);
-                        } else {
-                            v.x = swa::ex2(v.x);
-                            v.y = swa::ex2(v.y);
-                        }
+                        v.x = swa::ex2(v.x);
+                        v.y = swa::ex2(v.y);
                         sum = swa::add2(sum, v);
                         pk[c][e / 2] = __uint_as_float(swa::pack_bf16(v.x, v.y));
                     }
