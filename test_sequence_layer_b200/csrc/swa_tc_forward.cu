@@ -1,8 +1,9 @@
 // swa_tc_forward.cu -- sliding-window attention forward on the tensor cores
 // (bf16, d = 64 or 128).
 //
-// A CTA owns two tiles of 128 queries and walks the 128-key tiles that either
-// may see: the sinks, then the window. The pair is two heads that share keys
+// One CTA per SM takes pairs of 128-query tiles in turn and walks the 128-key
+// tiles that either may see: the sinks, then the window; the copies of the next
+// pair run under the products of the present one. The pair is two heads that share keys
 // where the group allows it, else two consecutive tiles of one head, so that
 // every key tile fetched serves two products. One warp issues the tile copies,
 // one the products, and eight warps per query tile do the softmax, two threads
@@ -74,22 +75,23 @@ template <int D> struct FwdSmem {
     static constexpr int oRing = 2 * kTile;          // K and V tiles, in turn
     static constexpr int oRow = oRing + kStages * kPiece;    // [2 tiles][128] floats
     static constexpr int oBar = oRow + 1024;
-    static constexpr int bytes = oBar + (2 * kStages + 8) * 8 + 16 + 1008;   // + slack to align the base
+    static constexpr int bytes = oBar + (2 * kStages + 9) * 8 + 16 + 1008;   // + slack to align the base
     static_assert(bytes <= 227 * 1024, "more than a CTA has");
 };
 
 struct FwdParams {
     SwaArgs a;
     int pair_heads;      // 1: the two tiles are heads 2 i, 2 i + 1 of one group; 0: consecutive tiles of one head
+    int nx, items;       // pairs along the queries, pairs in all
     unsigned* err;
 };
 
-// One query tile as every role of the CTA sees it.
+// One query tile of an item as every role of the CTA sees it.
 struct QueryTile {
     int head, t0, p0, p1;                            // flat query head, first query, first and last position
     bool live;
-    __device__ __forceinline__ QueryTile(const FwdParams& f, int x) {
-        const int blk = blockIdx.x, y = blockIdx.y;
+    __device__ __forceinline__ QueryTile(const FwdParams& f, int item, int x) {
+        const int blk = item % f.nx, y = item / f.nx;
         head = f.pair_heads ? 2 * y + x : y;
         t0 = (f.pair_heads ? blk : 2 * blk + x) * kQ;
         live = t0 < f.a.T;
@@ -110,25 +112,25 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::oBar);
     uint64_t* empty = full + L::kStages;
-    uint64_t* bar_q = empty + L::kStages;
-    uint64_t* s_full = bar_q + 1;                    // [2] scores of tile x are in tensor memory
+    uint64_t* bar_q = empty + L::kStages;            // the item's query tiles have landed
+    uint64_t* q_free = bar_q + 1;                    // its scores are done
+    uint64_t* s_full = q_free + 1;                   // [2] scores of tile x are in tensor memory
     uint64_t* p_full = s_full + 2;                   // [2] weights of tile x are
-    uint64_t* o_full = p_full + 2;                   // all products done
-    uint32_t* slot = reinterpret_cast<uint32_t*>(o_full + 1);
+    uint64_t* o_full = p_full + 2;                   // all products of the item done
+    uint64_t* o_free = o_full + 1;                   // every warp is through with the item
+    uint32_t* slot = reinterpret_cast<uint32_t*>(o_free + 1);
     float* rows = reinterpret_cast<float*>(smem + L::oRow);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const SwaArgs& a = f.a;
-    const QueryTile q0(f, 0), q1(f, 1);
-    const swa::KeyTiles kt(q0.p0, q1.live ? q1.p1 : q0.p1, a.window, a.sinks, kK);
-    const int hkv = q0.head / (a.Hq / a.Hkv);        // heads of one sequence follow one another: also flat
-
     if (tid == 0) {
         for (int i = 0; i < L::kStages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         mbar_init(bar_q, 1);
+        mbar_init(q_free, 1);
         mbar_init(o_full, 1);
+        mbar_init(o_free, kSoftmaxWarps);
         for (int x = 0; x < 2; ++x) {
             mbar_init(&s_full[x], 1);
             mbar_init(&p_full[x], 8);
@@ -146,20 +148,27 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
     if (warp == kSoftmaxWarps) {
         if (lane == 0) {
             // ---- copies: the query tiles, then K and V of every key tile ----
-            mbar_arrive_expect_tx(bar_q, 2 * L::kTile);
-            for (int x = 0; x < 2; ++x) {
-                const QueryTile& q = x ? q1 : q0;
-                for (int c = 0; c < D / 64; ++c)
-                    swa::tma_load(smem + L::oQ + x * L::kTile + c * 16384, &mq, c * 64, q.t0, q.head, bar_q);
-            }
-            for (int i = 0; i < 2 * kt.n && ok; ++i) {
-                const int st = i % L::kStages;
-                ok = mbar_wait(&empty[st], ((i / L::kStages) & 1) ^ 1);
+            int st = 0, ph = 1, k = 0;
+            for (int w = blockIdx.x; w < f.items && ok; w += gridDim.x, ++k) {
+                const QueryTile q0(f, w, 0), q1(f, w, 1);
+                const swa::KeyTiles kt(q0.p0, q1.live ? q1.p1 : q0.p1, a.window, a.sinks, kK);
+                const int hkv = q0.head / (a.Hq / a.Hkv);            // heads of one sequence follow one another
+                ok = swa::wait_bar(q_free, (k & 1) ^ 1);
                 if (!ok) break;
-                mbar_arrive_expect_tx(&full[st], L::kPiece);
-                for (int c = 0; c < D / 64; ++c)
-                    swa::tma_load(smem + L::oRing + st * L::kPiece + c * L::kBlock, (i & 1) ? &mv : &mk, c * 64,
-                                  kt.tile(i >> 1) * kK, hkv, &full[st]);
+                mbar_arrive_expect_tx(bar_q, 2 * L::kTile);
+                for (int x = 0; x < 2; ++x)
+                    for (int c = 0; c < D / 64; ++c)
+                        swa::tma_load(smem + L::oQ + x * L::kTile + c * 16384, &mq, c * 64, x ? q1.t0 : q0.t0,
+                                      x ? q1.head : q0.head, bar_q);
+                for (int i = 0; i < 2 * kt.n && ok; ++i) {
+                    ok = swa::wait_bar(&empty[st], ph);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&full[st], L::kPiece);
+                    for (int c = 0; c < D / 64; ++c)
+                        swa::tma_load(smem + L::oRing + st * L::kPiece + c * L::kBlock, (i & 1) ? &mv : &mk, c * 64,
+                                      kt.tile(i >> 1) * kK, hkv, &full[st]);
+                    if (++st == L::kStages) st = 0, ph ^= 1;
+                }
             }
         }
     } else if (warp > kSoftmaxWarps) {
@@ -171,6 +180,7 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
             const uint64_t dk = sdesc(smem_addr(smem + L::oRing), 0, 1024);
             const uint64_t dv = sdesc(smem_addr(smem + L::oRing), L::kBlock, 1024);
             uint32_t np[2] = {0, 0};                 // weights taken so far, per tile
+            bool first[2] = {true, true};            // of the item
             int st = 0, ph = 0;                      // ring stage of the next tile to take, its phase
             auto next_stage = [&]() {
                 if (++st == L::kStages) st = 0, ph ^= 1;
@@ -188,52 +198,61 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
 #pragma unroll
                 for (int s = 0; s < kK / 16; ++s)
                     swa::mma_ts(tm + 256 + 128 * x, tm + 128 * x + 8 * s, dv + ((stage * L::kPiece + s * 2048) >> 4), idO,
-                                np[x] > 0 || s > 0);
+                                !first[x] || s > 0);
+                first[x] = false;
                 ++np[x];
             };
-            ok = swa::wait_bar(bar_q, 0) && swa::wait_bar(&full[0], 0);
-            bool use[2] = {q0.uses(kt.tile(0) * kK, a.window, a.sinks), q1.uses(kt.tile(0) * kK, a.window, a.sinks)};
-            if (ok) {
-                if (use[0]) scores(0, 0);
-                if (use[1]) scores(1, 0);
-                mma_commit(&empty[0]);
-            }
-            next_stage();
-            for (int it = 0; it < kt.n && ok; ++it) {
-                const bool more = it + 1 < kt.n;
-                const int jn = kt.tile(it + 1) * kK;
-                const bool next[2] = {more && q0.uses(jn, a.window, a.sinks), more && q1.uses(jn, a.window, a.sinks)};
-                const int sv = st;
-                ok = swa::wait_bar(&full[st], ph);
+            int k = 0;
+            for (int w = blockIdx.x; w < f.items && ok; w += gridDim.x, ++k) {
+                const QueryTile q0(f, w, 0), q1(f, w, 1);
+                const swa::KeyTiles kt(q0.p0, q1.live ? q1.p1 : q0.p1, a.window, a.sinks, kK);
+                ok = swa::wait_bar(bar_q, k & 1) && swa::wait_bar(&full[st], ph);
+                if (!ok) break;
+                bool use[2] = {q0.uses(kt.tile(0) * kK, a.window, a.sinks), q1.uses(kt.tile(0) * kK, a.window, a.sinks)};
+                first[0] = first[1] = true;
+                // the last item's weights have been taken, in order
+                if (use[0]) scores(0, st);
+                if (use[1]) scores(1, st);
+                mma_commit(&empty[st]);
                 next_stage();
-                if (more) ok = ok && swa::wait_bar(&full[st], ph);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (use[x] && ok) {
-                        ok = swa::wait_bar(&p_full[x], np[x] & 1);
-                        tc_fence_after();
-                        if (ok) values(x, sv);
-                    }
-                    if (x == 1) mma_commit(&empty[sv]);
-                    if (next[x] && ok) scores(x, st);
-                    use[x] = next[x];
-                }
-                if (more) {
-                    mma_commit(&empty[st]);
+                for (int it = 0; it < kt.n && ok; ++it) {
+                    const bool more = it + 1 < kt.n;
+                    const int jn = kt.tile(it + 1) * kK;
+                    const bool next[2] = {more && q0.uses(jn, a.window, a.sinks), more && q1.uses(jn, a.window, a.sinks)};
+                    const int sv = st;
+                    ok = swa::wait_bar(&full[st], ph);
                     next_stage();
+                    if (more) ok = ok && swa::wait_bar(&full[st], ph);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (use[x] && ok) {
+                            ok = swa::wait_bar(&p_full[x], np[x] & 1);
+                            tc_fence_after();
+                            if (ok) values(x, sv);
+                        }
+                        if (x == 1) mma_commit(&empty[sv]);
+                        if (next[x] && ok) scores(x, st);
+                        use[x] = next[x];
+                    }
+                    if (more) {
+                        mma_commit(&empty[st]);
+                        next_stage();
+                    }
                 }
+                mma_commit(q_free);
+                // nobody is left an item behind: a parity tells only two phases apart
+                if (k > 0 && ok) ok = swa::wait_bar(o_free, (k - 1) & 1);
+                mma_commit(o_full);
             }
-            mma_commit(o_full);
             // leave only when nothing is in flight any more
-            mbar_wait(o_full, 0);
+            if (k > 0) mbar_wait(o_full, (k - 1) & 1);
         }
     } else {
         // ---- softmax of tile x: columns 64 half .. of a row per thread. A
         // thread that gave up a wait goes on without waiting, so that the
         // others' barriers are met. ----
         const int x = warp >> 3, half = (warp >> 2) & 1;
-        const QueryTile q(f, x);
-        const int row = (warp & 3) * 32 + lane, pos = q.p0 + row;
+        const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tm + 128 * x + lanes, tO = tm + 256 + 128 * x + half * (D / 2) + lanes;
         float* shared_row = rows + x * kQ + row;     // between the two threads of a row
@@ -247,118 +266,126 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         const float sc = a.scale * swa::kLog2e;
         constexpr float kLimit = 256.f;
         const float2 sc2 = make_float2(sc, sc);
-        float m = -INFINITY;
-        float2 l2 = make_float2(0.f, 0.f);
         uint32_t n = 0;
-        for (int it = 0; it < kt.n; ++it) {
-            const int j0 = kt.tile(it) * kK;
-            if (!q.uses(j0, a.window, a.sinks)) continue;
-            if (ok) ok = swa::wait_bar(&s_full[x], n & 1);
-            tc_fence_after();
-            float s[2][32], pk[2][16];
-            const bool whole = j0 + kK - 1 <= q.p0 && q.p0 + kQ - 1 - j0 < a.window;
-            auto fetch = [&]() {
-                tmem_ld32_x32(tS + 64 * half, s[0]);
-                tmem_ld32_x32(tS + 64 * half + 32, s[1]);
-                tmem_wait_ld();
-                if (whole) return;
-                const int c0 = j0 + 64 * half;
-                const int hi = pos - c0, lo = pos - a.window + 1 - c0, sk = a.sinks - c0;
+        int k = 0;
+        for (int w = blockIdx.x; w < f.items; w += gridDim.x, ++k) {
+            const QueryTile q0(f, w, 0), q1(f, w, 1), q(f, w, x);
+            const swa::KeyTiles kt(q0.p0, q1.live ? q1.p1 : q0.p1, a.window, a.sinks, kK);
+            const int pos = q.p0 + row;
+            float m = -INFINITY;
+            float2 l2 = make_float2(0.f, 0.f);
+            for (int it = 0; it < kt.n; ++it) {
+                const int j0 = kt.tile(it) * kK;
+                if (!q.uses(j0, a.window, a.sinks)) continue;
+                if (ok) ok = swa::wait_bar(&s_full[x], n & 1);
+                tc_fence_after();
+                float s[2][32], pk[2][16];
+                const bool whole = j0 + kK - 1 <= q.p0 && q.p0 + kQ - 1 - j0 < a.window;
+                auto fetch = [&]() {
+                    tmem_ld32_x32(tS + 64 * half, s[0]);
+                    tmem_ld32_x32(tS + 64 * half + 32, s[1]);
+                    tmem_wait_ld();
+                    if (whole) return;
+                    const int c0 = j0 + 64 * half;
+                    const int hi = pos - c0, lo = pos - a.window + 1 - c0, sk = a.sinks - c0;
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int j = 32 * c + e;
-                        if (!(j <= hi && (j >= lo || j < sk))) s[c][e] = -INFINITY;
+                        for (int e = 0; e < 32; ++e) {
+                            const int j = 32 * c + e;
+                            if (!(j <= hi && (j >= lo || j < sk))) s[c][e] = -INFINITY;
+                        }
+                };
+                fetch();
+                float2 sum = make_float2(0.f, 0.f);
+                auto weigh = [&](float neg) {
+                    const float2 neg2 = make_float2(neg, neg);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float2 v = swa::fma2(make_float2(s[c][e], s[c][e + 1]), sc2, neg2);
+                            v.x = swa::ex2(v.x);
+                            v.y = swa::ex2(v.y);
+                            sum = swa::add2(sum, v);
+                            pk[c][e / 2] = __uint_as_float(swa::pack_bf16(v.x, v.y));
+                        }
+                };
+                weigh(-m * sc);
+                // the tile's threads agree on it, and have all read their scores; a row
+                // moves its reference on its own weights alone
+                const bool passed = !(sum.x + sum.y <= kLimit);
+                if (swa::bar_any(1 + x, 256, passed)) {
+                    fetch();                             // the weights took the scores' registers
+                    float top = s[0][0];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(s[c][e], s[c][e + 1]));
+                    auto larger = [](float u, float v) { return fmaxf(u, v); };
+                    const bool move = exchange(passed ? 1.f : 0.f, larger) > 0.f;
+                    top = exchange(top, larger);
+                    float keep = 1.f;
+                    if (m == -INFINITY) {
+                        m = top;                         // O and l hold nothing yet
+                    } else if (move && top > m) {
+                        keep = swa::ex2((m - top) * sc);
+                        m = top;
                     }
-            };
-            fetch();
-            float2 sum = make_float2(0.f, 0.f);
-            auto weigh = [&](float neg) {
-                const float2 neg2 = make_float2(neg, neg);
+                    if (__any_sync(~0u, keep != 1.f)) {
+                        // S(n) is complete, so P V(n - 1), issued before it, is too
+                        l2.x *= keep;
+                        l2.y *= keep;
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                        for (int c = 0; c < D / 2; c += 16) {
+                            float o[16];
+                            tmem_ld32_x16(tO + c, o);
+                            tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float2 v = swa::fma2(make_float2(s[c][e], s[c][e + 1]), sc2, neg2);
-                        v.x = swa::ex2(v.x);
-                        v.y = swa::ex2(v.y);
-                        sum = swa::add2(sum, v);
-                        pk[c][e / 2] = __uint_as_float(swa::pack_bf16(v.x, v.y));
+                            for (int e = 0; e < 16; ++e) o[e] *= keep;
+                            tmem_st32_x16(tO + c, o);
+                        }
                     }
-            };
-            weigh(-m * sc);
-            // the tile's threads agree on it, and have all read their scores; a row
-            // moves its reference on its own weights alone
-            const bool passed = !(sum.x + sum.y <= kLimit);
-            if (swa::bar_any(1 + x, 256, passed)) {
-                fetch();                             // the weights took the scores' registers
-                float top = s[0][0];
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(s[c][e], s[c][e + 1]));
-                auto larger = [](float u, float v) { return fmaxf(u, v); };
-                const bool move = exchange(passed ? 1.f : 0.f, larger) > 0.f;
-                top = exchange(top, larger);
-                float keep = 1.f;
-                if (m == -INFINITY) {
-                    m = top;                         // O and l hold nothing yet
-                } else if (move && top > m) {
-                    keep = swa::ex2((m - top) * sc);
-                    m = top;
+                    sum = make_float2(0.f, 0.f);
+                    weigh(m == -INFINITY ? 0.f : -m * sc);
                 }
-                if (__any_sync(~0u, keep != 1.f)) {
-                    // S(n) is complete, so P V(n - 1), issued before it, is too
-                    l2.x *= keep;
-                    l2.y *= keep;
-#pragma unroll
-                    for (int c = 0; c < D / 2; c += 16) {
-                        float o[16];
-                        tmem_ld32_x16(tO + c, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] *= keep;
-                        tmem_st32_x16(tO + c, o);
-                    }
-                }
-                sum = make_float2(0.f, 0.f);
-                weigh(m == -INFINITY ? 0.f : -m * sc);
+                tmem_st32_x16(tS + 32 * half, pk[0]);
+                tmem_st32_x16(tS + 32 * half + 16, pk[1]);
+                l2 = swa::add2(l2, sum);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) swa::mbar_arrive(&p_full[x]);
+                ++n;
             }
-            tmem_st32_x16(tS + 32 * half, pk[0]);
-            tmem_st32_x16(tS + 32 * half + 16, pk[1]);
-            l2 = swa::add2(l2, sum);
-            tmem_wait_st();
-            tc_fence_before();
+            // ---- output ----
+            if (q.live) {
+                const float l = exchange(l2.x + l2.y, [](float u, float v) { return u + v; }), inv = 1.f / l;
+                if (ok) ok = swa::wait_bar(o_full, k & 1);
+                tc_fence_after();
+                const int tq = q.t0 + row;
+                const bool in = tq < a.T && ok;
+                const size_t r = (size_t)q.head * a.T + tq;
+#pragma unroll
+                for (int c = 0; c < D / 2; c += 32) {
+                    float o[32];
+                    tmem_ld32_x32(tO + c, o);
+                    tmem_wait_ld();
+                    if (in) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + r * D + half * (D / 2) + c);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            dst[e / 8] = make_uint4(swa::pack_bf16(o[e] * inv, o[e + 1] * inv),
+                                                    swa::pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                                                    swa::pack_bf16(o[e + 4] * inv, o[e + 5] * inv),
+                                                    swa::pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+                    }
+                }
+                if (in && half == 0 && a.lse) a.lse[r] = fmaf(m, a.scale, logf(l));
+                tc_fence_before();
+            }
             __syncwarp();
-            if (lane == 0) swa::mbar_arrive(&p_full[x]);
-            ++n;
-        }
-        // ---- output ----
-        if (q.live) {
-            const float l = exchange(l2.x + l2.y, [](float u, float v) { return u + v; }), inv = 1.f / l;
-            if (ok) ok = mbar_wait(o_full, 0);
-            tc_fence_after();
-            const int tq = q.t0 + row;
-            const bool in = tq < a.T && ok;
-            const size_t r = (size_t)q.head * a.T + tq;
-#pragma unroll
-            for (int c = 0; c < D / 2; c += 32) {
-                float o[32];
-                tmem_ld32_x32(tO + c, o);
-                tmem_wait_ld();
-                if (in) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + r * D + half * (D / 2) + c);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        dst[e / 8] = make_uint4(swa::pack_bf16(o[e] * inv, o[e + 1] * inv),
-                                                swa::pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
-                                                swa::pack_bf16(o[e + 4] * inv, o[e + 5] * inv),
-                                                swa::pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
-                }
-            }
-            if (in && half == 0 && a.lse) a.lse[r] = fmaf(m, a.scale, logf(l));
-            tc_fence_before();
+            if (lane == 0) swa::mbar_arrive(o_free);
         }
     }
     if (!ok) record_error(f.err, kErrTimeout);
@@ -373,13 +400,14 @@ cudaError_t launch(const SwaArgs& a, cudaStream_t st) {
     if (!swa::make_map(&mq, a.q, D, a.T, a.B * a.Hq, kQ) || !swa::make_map(&mk, a.k, D, a.S, a.B * a.Hkv, kK) ||
         !swa::make_map(&mv, a.v, D, a.S, a.B * a.Hkv, kK))
         return cudaErrorInvalidValue;
-    FwdParams f{a, (a.Hq / a.Hkv) % 2 == 0 ? 1 : 0, error_word_ptr()};
+    const int tiles = (a.T + kQ - 1) / kQ, pair_heads = (a.Hq / a.Hkv) % 2 == 0 ? 1 : 0;
+    const int nx = pair_heads ? tiles : (tiles + 1) / 2, ny = a.B * a.Hq / (pair_heads ? 2 : 1);
+    if ((long long)nx * ny > 0x7fffffffLL) return cudaErrorInvalidValue;
+    FwdParams f{a, pair_heads, nx, nx * ny, error_word_ptr()};
     if (!f.err) return cudaErrorUnknown;
     cudaError_t e = cudaFuncSetAttribute(swa_tc_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes);
     if (e != cudaSuccess) return e;
-    const int tiles = (a.T + kQ - 1) / kQ;
-    const dim3 grid = f.pair_heads ? dim3(tiles, a.B * a.Hq / 2) : dim3((tiles + 1) / 2, a.B * a.Hq);
-    swa_tc_fwd_kernel<D><<<grid, kFwdThreads, L::bytes, st>>>(mq, mk, mv, f);
+    swa_tc_fwd_kernel<D><<<f.items < 148 ? f.items : 148, kFwdThreads, L::bytes, st>>>(mq, mk, mv, f);
     return cudaGetLastError();
 }
 
