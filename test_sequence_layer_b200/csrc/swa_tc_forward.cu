@@ -103,6 +103,13 @@ struct QueryTile {
     }
 };
 
+// the n lowest bits
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+// Newest keys first: a query tile begins on its diagonal, where every row sees a
+// key (where S - T is no multiple of the tile, at the second step at the latest).
+__device__ __forceinline__ int key_tile(const swa::KeyTiles& kt, int i) { return kt.tile(kt.n - 1 - i); }
+
 template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -166,7 +173,7 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                     mbar_arrive_expect_tx(&full[st], L::kPiece);
                     for (int c = 0; c < D / 64; ++c)
                         swa::tma_load(smem + L::oRing + st * L::kPiece + c * L::kBlock, (i & 1) ? &mv : &mk, c * 64,
-                                      kt.tile(i >> 1) * kK, hkv, &full[st]);
+                                      key_tile(kt, i >> 1) * kK, hkv, &full[st]);
                     if (++st == L::kStages) st = 0, ph ^= 1;
                 }
             }
@@ -208,7 +215,8 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 const swa::KeyTiles kt(q0.p0, q1.live ? q1.p1 : q0.p1, a.window, a.sinks, kK);
                 ok = swa::wait_bar(bar_q, k & 1) && swa::wait_bar(&full[st], ph);
                 if (!ok) break;
-                bool use[2] = {q0.uses(kt.tile(0) * kK, a.window, a.sinks), q1.uses(kt.tile(0) * kK, a.window, a.sinks)};
+                bool use[2] = {q0.uses(key_tile(kt, 0) * kK, a.window, a.sinks),
+                               q1.uses(key_tile(kt, 0) * kK, a.window, a.sinks)};
                 first[0] = first[1] = true;
                 // the last item's weights have been taken, in order
                 if (use[0]) scores(0, st);
@@ -217,7 +225,7 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 next_stage();
                 for (int it = 0; it < kt.n && ok; ++it) {
                     const bool more = it + 1 < kt.n;
-                    const int jn = kt.tile(it + 1) * kK;
+                    const int jn = key_tile(kt, it + 1) * kK;
                     const bool next[2] = {more && q0.uses(jn, a.window, a.sinks), more && q1.uses(jn, a.window, a.sinks)};
                     const int sv = st;
                     ok = swa::wait_bar(&full[st], ph);
@@ -272,10 +280,11 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
             const QueryTile q0(f, w, 0), q1(f, w, 1), q(f, w, x);
             const swa::KeyTiles kt(q0.p0, q1.live ? q1.p1 : q0.p1, a.window, a.sinks, kK);
             const int pos = q.p0 + row;
+            bool begin = true;                       // the same for all threads of a tile
             float m = -INFINITY;
             float2 l2 = make_float2(0.f, 0.f);
             for (int it = 0; it < kt.n; ++it) {
-                const int j0 = kt.tile(it) * kK;
+                const int j0 = key_tile(kt, it) * kK;
                 if (!q.uses(j0, a.window, a.sinks)) continue;
                 if (ok) ok = swa::wait_bar(&s_full[x], n & 1);
                 tc_fence_after();
@@ -286,15 +295,16 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                     tmem_ld32_x32(tS + 64 * half + 32, s[1]);
                     tmem_wait_ld();
                     if (whole) return;
+                    // bit e of a word: column 32 c + e is visible
                     const int c0 = j0 + 64 * half;
                     const int hi = pos - c0, lo = pos - a.window + 1 - c0, sk = a.sinks - c0;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t vis = below(hi + 1 - 32 * c) & (~below(lo - 32 * c) | below(sk - 32 * c));
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int j = 32 * c + e;
-                            if (!(j <= hi && (j >= lo || j < sk))) s[c][e] = -INFINITY;
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (!(vis & (1u << e))) s[c][e] = -INFINITY;
+                    }
                 };
                 fetch();
                 float2 sum = make_float2(0.f, 0.f);
@@ -311,43 +321,52 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                             pk[c][e / 2] = __uint_as_float(swa::pack_bf16(v.x, v.y));
                         }
                 };
-                weigh(-m * sc);
-                // the tile's threads agree on it, and have all read their scores; a row
-                // moves its reference on its own weights alone
-                const bool passed = !(sum.x + sum.y <= kLimit);
-                if (swa::bar_any(1 + x, 256, passed)) {
-                    fetch();                             // the weights took the scores' registers
-                    float top = s[0][0];
+                auto row_max = [&]() {
+                    float t[4];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < 4; ++c) {
+                        t[c] = s[c / 2][16 * (c & 1)];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(s[c][e], s[c][e + 1]));
-                    auto larger = [](float u, float v) { return fmaxf(u, v); };
-                    const bool move = exchange(passed ? 1.f : 0.f, larger) > 0.f;
-                    top = exchange(top, larger);
-                    float keep = 1.f;
-                    if (m == -INFINITY) {
-                        m = top;                         // O and l hold nothing yet
-                    } else if (move && top > m) {
-                        keep = swa::ex2((m - top) * sc);
-                        m = top;
+                        for (int e = 1; e < 16; ++e) t[c] = fmaxf(t[c], s[c / 2][16 * (c & 1) + e]);
                     }
-                    if (__any_sync(~0u, keep != 1.f)) {
-                        // S(n) is complete, so P V(n - 1), issued before it, is too
-                        l2.x *= keep;
-                        l2.y *= keep;
-#pragma unroll
-                        for (int c = 0; c < D / 2; c += 16) {
-                            float o[16];
-                            tmem_ld32_x16(tO + c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= keep;
-                            tmem_st32_x16(tO + c, o);
-                        }
-                    }
-                    sum = make_float2(0.f, 0.f);
+                    return exchange(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])),
+                                    [](float u, float v) { return fmaxf(u, v); });
+                };
+                if (begin) {
+                    begin = false;
+                    m = row_max();
                     weigh(m == -INFINITY ? 0.f : -m * sc);
+                } else {
+                    weigh(-m * sc);                  // NaN in a row that has seen no key yet
+                    // the tile's threads agree on it, and have all read their scores; a
+                    // row moves its reference on its own weights alone
+                    const bool passed = !(sum.x + sum.y <= kLimit);
+                    if (swa::bar_any(1 + x, 256, passed)) {
+                        fetch();                     // the weights took the scores' registers
+                        const bool move = exchange(passed ? 1.f : 0.f, [](float u, float v) { return fmaxf(u, v); }) > 0.f;
+                        const float top = row_max();
+                        float keep = 1.f;
+                        if (move && top > m) {
+                            keep = swa::ex2((m - top) * sc);
+                            m = top;
+                        }
+                        if (__any_sync(~0u, keep != 1.f)) {
+                            // S(n) is complete, so P V(n - 1), issued before it, is too
+                            l2.x *= keep;
+                            l2.y *= keep;
+#pragma unroll
+                            for (int c = 0; c < D / 2; c += 16) {
+                                float o[16];
+                                tmem_ld32_x16(tO + c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] *= keep;
+                                tmem_st32_x16(tO + c, o);
+                            }
+                        }
+                        sum = make_float2(0.f, 0.f);
+                        weigh(m == -INFINITY ? 0.f : -m * sc);
+                    }
                 }
                 tmem_st32_x16(tS + 32 * half, pk[0]);
                 tmem_st32_x16(tS + 32 * half + 16, pk[1]);
