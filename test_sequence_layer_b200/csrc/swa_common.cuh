@@ -14,6 +14,9 @@ __device__ __forceinline__ bool visible(int p, int j, int window, int sinks) {
     return j <= p && (p - j < window || j < sinks);
 }
 
+// the n lowest bits of a word
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
 // The key tiles (of `bn` keys) that queries at positions [p0, p1] may see: the
 // sink tiles [0, n_sink) and the window tiles [first, last], without overlap.
 struct KeyTiles {

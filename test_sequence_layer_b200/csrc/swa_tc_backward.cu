@@ -70,9 +70,9 @@ __device__ __forceinline__ uint8_t* align_smem(uint8_t* p) {
 }
 
 // 32 columns of scores and of dP -> 32 columns of P and dS, packed to bf16.
-// st(e): the column's (lse log2 e, delta).
+// st(e): the column's (lse log2 e, delta). Bit e of `vis`: it is visible.
 template <bool kWantP, typename Stat>
-__device__ __forceinline__ void weights32(const float (&s)[32], const float (&dp)[32], float sc, int lo, int hi,
+__device__ __forceinline__ void weights32(const float (&s)[32], const float (&dp)[32], float sc, uint32_t vis,
                                           bool whole, Stat st, float (&pk)[16], float (&dk)[16]) {
     const float2 sc2 = make_float2(sc, sc);
 #pragma unroll
@@ -82,8 +82,8 @@ __device__ __forceinline__ void weights32(const float (&s)[32], const float (&dp
         w.x = swa::ex2(w.x);
         w.y = swa::ex2(w.y);
         if (!whole) {
-            if (e < lo || e >= hi) w.x = 0.f;
-            if (e + 1 < lo || e + 1 >= hi) w.y = 0.f;
+            if (!(vis & (1u << e))) w.x = 0.f;
+            if (!(vis & (2u << e))) w.y = 0.f;
         }
         const float2 g = swa::mul2(w, swa::add2(make_float2(dp[e], dp[e + 1]), make_float2(-a.y, -b.y)));
         if (kWantP) pk[e / 2] = __uint_as_float(swa::pack_bf16(w.x, w.y));
@@ -255,14 +255,10 @@ swa_tc_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             for (int c = 0; c < 2; ++c) {
                 const int base = j0 + 64 * half + 32 * c;
                 float pk[16], ds[16];
-                if (!whole) {
-                    // the visible keys of a row are [0, sinks) and (pos - window, pos]
-                    const int hi = pos + 1 - base, lo = pos - a.window + 1 - base, sk = min(a.sinks - base, hi);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!(e < hi && (e >= lo || e < sk))) s[c][e] = -INFINITY;
-                }
-                weights32<false>(s[c], dp[c], sc, 0, 32, true, [&](int) { return stat; }, pk, ds);
+                // the visible keys of a row are [0, sinks) and (pos - window, pos]
+                const uint32_t vis = swa::below(pos + 1 - base) &
+                                     (~swa::below(pos - a.window + 1 - base) | swa::below(a.sinks - base));
+                weights32<false>(s[c], dp[c], sc, vis, whole, [&](int) { return stat; }, pk, ds);
                 tmem_st32_x16(tS + 64 * half + 16 * c, ds);         // over columns this thread has read
             }
             tmem_wait_st();
@@ -420,7 +416,8 @@ swa_tc_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 tmem_ld32_x32(tS + 32 * c, s);
                 tmem_ld32_x32(tS + 64 + 32 * c, dp);
                 tmem_wait_ld();
-                weights32<true>(s, dp, sc, lo - 32 * c, hi - 32 * c, whole, [&](int e) { return stat[32 * c + e]; }, pk, ds);
+                weights32<true>(s, dp, sc, swa::below(hi - 32 * c) & ~swa::below(lo - 32 * c), whole,
+                                [&](int e) { return stat[32 * c + e]; }, pk, ds);
                 tmem_st32_x16(tS + 16 * c, pk);      // over columns already read
                 tmem_st32_x16(tS + 64 + 16 * c, ds);
             }

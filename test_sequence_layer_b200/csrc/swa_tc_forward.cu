@@ -103,9 +103,6 @@ struct QueryTile {
     }
 };
 
-// the n lowest bits
-__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
-
 // Newest keys first: a query tile begins on its diagonal, where every row sees a
 // key (where S - T is no multiple of the tile, at the second step at the latest).
 __device__ __forceinline__ int key_tile(const swa::KeyTiles& kt, int i) { return kt.tile(kt.n - 1 - i); }
@@ -300,7 +297,7 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                     const int hi = pos - c0, lo = pos - a.window + 1 - c0, sk = a.sinks - c0;
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const uint32_t vis = below(hi + 1 - 32 * c) & (~below(lo - 32 * c) | below(sk - 32 * c));
+                        const uint32_t vis = swa::below(hi + 1 - 32 * c) & (~swa::below(lo - 32 * c) | swa::below(sk - 32 * c));
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (!(vis & (1u << e))) s[c][e] = -INFINITY;
