@@ -9,7 +9,7 @@
 // but would have to add up dq across CTAs with atomics, whose order changes
 // the result. Sums stay in fp32 in tensor memory; P and dS are rounded to bf16
 // as the left operands of their products, which read them from tensor memory.
-// swa_stats_kernel first forms (lse log2 e, delta) per query, padded to whole
+// swa_stats_kernel first forms (lse log2 e, delta) for every query, padded to whole
 // tiles with lse = +inf, so that rows past the end weigh nothing.
 //
 // The tile that holds the sinks is seen by every query: its query range is cut
@@ -41,28 +41,58 @@ struct BwdParams {
 };
 
 // ---- (lse log2 e, delta) per query ----
-template <int D>
-__global__ void swa_stats_kernel(const __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __restrict__ dout,
-                                 const float* __restrict__ lse, int T, int tpad, float2* __restrict__ stats) {
+// delta = rowsum(dout o out) takes out as rounded to bf16. With a handful of
+// visible keys dP - delta is small against delta, and that rounding would show
+// (twice the error of dS's own rounding at two keys, a half at eight); up to
+// kFewKeys of them delta is summed from the weights instead, sum_j P_j dP_j.
+constexpr int kFewKeys = 8;
+
+__device__ __forceinline__ float dot8(const uint4& x, const uint4& y) {
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), s);
+        s = fmaf(__uint_as_float(xs[i] & 0xffff0000u), __uint_as_float(ys[i] & 0xffff0000u), s);
+    }
+    return s;
+}
+
+template <int D, bool FEW>
+__global__ void swa_stats_kernel(SwaArgs a, const __nv_bfloat16* __restrict__ dout, int tpad, float2* __restrict__ stats) {
+    using bf = __nv_bfloat16;
     constexpr int kLanes = D / 8;                    // 16-byte pieces of a row
     const int row = (blockIdx.x * blockDim.x + threadIdx.x) / kLanes, piece = threadIdx.x % kLanes;
     if (row >= tpad) return;                         // whole groups of kLanes lanes
-    const size_t src = (size_t)blockIdx.y * T + row;
-    float s = 0.f;
-    if (row < T) {
-        const uint4 x = reinterpret_cast<const uint4*>(out + src * D)[piece];
-        const uint4 y = reinterpret_cast<const uint4*>(dout + src * D)[piece];
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    const bool in = row < a.T;
+    const size_t src = (size_t)blockIdx.y * a.T + (in ? row : 0);
+    auto sum = [&](float v) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), s);
-            s = fmaf(__uint_as_float(xs[i] & 0xffff0000u), __uint_as_float(ys[i] & 0xffff0000u), s);
+        for (int i = kLanes / 2; i; i >>= 1) v += __shfl_xor_sync(~0u, v, i);
+        return v;
+    };
+    const float lse2 = a.lse[src] * swa::kLog2e;
+    const uint4 g = reinterpret_cast<const uint4*>(dout + src * D)[piece];
+    float delta;
+    if (FEW) {
+        const size_t kv = (size_t)(blockIdx.y / (a.Hq / a.Hkv)) * a.S * D;
+        const uint4 q = reinterpret_cast<const uint4*>(static_cast<const bf*>(a.q) + src * D)[piece];
+        const int p = a.S - a.T + (in ? row : 0), lo = max(0, p - a.window + 1);
+        delta = 0.f;
+        // every lane of a warp runs kFewKeys steps: step i is sink i, then the window's keys
+        const int sinks = min(a.sinks, lo), n = sinks + p - lo + 1;
+#pragma unroll
+        for (int i = 0; i < kFewKeys; ++i) {
+            const int j = i < sinks ? i : min(lo + i - sinks, p);
+            const uint4 k = reinterpret_cast<const uint4*>(static_cast<const bf*>(a.k) + kv + (size_t)j * D)[piece];
+            const uint4 v = reinterpret_cast<const uint4*>(static_cast<const bf*>(a.v) + kv + (size_t)j * D)[piece];
+            const float w = swa::ex2(fmaf(sum(dot8(q, k)), a.scale * swa::kLog2e, -lse2)), dp = sum(dot8(g, v));
+            if (i < n) delta = fmaf(w, dp, delta);
         }
+    } else {
+        delta = sum(dot8(reinterpret_cast<const uint4*>(static_cast<const bf*>(a.out) + src * D)[piece], g));
     }
-#pragma unroll
-    for (int i = kLanes / 2; i; i >>= 1) s += __shfl_xor_sync(~0u, s, i);
-    if (piece == 0)
-        stats[(size_t)blockIdx.y * tpad + row] = make_float2(row < T ? lse[src] * swa::kLog2e : INFINITY, s);
+    if (piece == 0) stats[(size_t)blockIdx.y * tpad + row] = make_float2(in ? lse2 : INFINITY, in ? delta : 0.f);
 }
 
 __device__ __forceinline__ uint8_t* align_smem(uint8_t* p) {
@@ -513,8 +543,10 @@ cudaError_t launch(const SwaBackwardArgs& b, cudaStream_t st) {
         e = cudaFuncSetAttribute(swa_tc_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DkvSmem<D>::bytes);
     if (e != cudaSuccess) return e;
     const int rows = 256 / (D / 8);
-    swa_stats_kernel<D><<<dim3((f.tpad + rows - 1) / rows, a.B * a.Hq), 256, 0, st>>>(
-        static_cast<const __nv_bfloat16*>(a.out), static_cast<const __nv_bfloat16*>(b.dout), a.lse, a.T, f.tpad, stats);
+    const dim3 grid((f.tpad + rows - 1) / rows, a.B * a.Hq);
+    const __nv_bfloat16* dout = static_cast<const __nv_bfloat16*>(b.dout);
+    if (a.window + a.sinks <= kFewKeys) swa_stats_kernel<D, true><<<grid, 256, 0, st>>>(a, dout, f.tpad, stats);
+    else swa_stats_kernel<D, false><<<grid, 256, 0, st>>>(a, dout, f.tpad, stats);
     const int kt = (a.S + kTile - 1) / kTile;
     swa_tc_dkv_kernel<D><<<dim3(kt - 1 + f.chunks, a.B * a.Hkv), kThreads, DkvSmem<D>::bytes, st>>>(q64, do64, mk, mv, f);
     swa_tc_dq_kernel<D><<<dim3(f.tpad / kTile, a.B * a.Hq), kThreads, DqSmem<D>::bytes, st>>>(q128, do128, mk, mv, f);
