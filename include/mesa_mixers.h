@@ -12,6 +12,9 @@
  * pointers. Outputs must not overlap inputs or each other
  * (MESA_ERR_INVALID_ARG) unless stated otherwise. Every result is
  * bit-reproducible from call to call: no floating-point atomics are used.
+ * Make one call on a device before capturing calls into a graph there (the
+ * first looks up the device's error word). A kernel that gives up a bounded
+ * wait records MESA_ERR_DEVICE_TIMEOUT for mesa_get_error().
  */
 #ifndef MESA_MIXERS_H
 #define MESA_MIXERS_H

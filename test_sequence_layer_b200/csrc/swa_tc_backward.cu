@@ -266,7 +266,7 @@ swa_tc_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         const float sc = a.scale * swa::kLog2e;
         for (int n = 0; n < kt.n; ++n) {
             const int j0 = kt.tile(n) * kTile;
-            ok = swa::wait_bar(s_full, n & 1);
+            ok = __all_sync(~0u, swa::wait_bar(s_full, n & 1));      // a warp leaves as one
             if (!ok) break;
             tc_fence_after();
             const uint32_t tS = tm + 128 * (n & 1) + lanes;
@@ -433,6 +433,7 @@ swa_tc_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
             const int st = n % L::kStages, q0 = off + ta + (n % per) * kSub;
             ok = swa::wait_bar(&full[st], (n / L::kStages) & 1);             // the statistics
             ok = ok && swa::wait_bar(&s_full[grp], (n >> 1) & 1);
+            ok = __all_sync(~0u, ok);                                       // a warp leaves as one
             if (!ok) break;
             tc_fence_after();
             const uint32_t tS = tm + 128 * grp + lanes;

@@ -480,6 +480,8 @@ class _On:
         if stream is None:
             self.raw = torch._C._cuda_getCurrentRawStream(index)
         else:
+            if stream.device_index != index:
+                raise ValueError(f"stream belongs to cuda:{stream.device_index}, the tensors to cuda:{index}")
             self.contexts += (torch.cuda.stream(stream),)
             self.raw = stream.cuda_stream
 
