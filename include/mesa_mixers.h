@@ -118,7 +118,8 @@ mesa_status mesa_swa_forward(const void* q, const void* k, const void* v, int B,
  * (dk, dv summed over the query heads that share a head).
  *   dq [B,Hq,T,d];  dk, dv [B,Hkv,S,d]; all in `dtype`, rounded once.
  *   workspace    mesa_swa_backward_workspace_size() bytes, 256-byte aligned.
- * Keys that no query sees get zero gradients (T < S, or T = 0).
+ * Keys that no query sees get zero gradients (T < S, or T = 0); where every
+ * query sees one key alone, dq and dk are exactly zero.
  */
 size_t mesa_swa_backward_workspace_size(int B, int Hq, int Hkv, int T, int S, int d, int sinks, mesa_dtype dtype);
 mesa_status mesa_swa_backward(const void* q, const void* k, const void* v, const void* out, const float* lse,

@@ -207,7 +207,14 @@ mesa_status mesa_swa_backward(const void* q, const void* k, const void* v, const
     SwaArgs f{q, k, v, B, Hq, Hkv, T, S, d, window < S ? window : S, sinks, scale, dtype,
               const_cast<void*>(out), const_cast<float*>(lse)};
     SwaBackwardArgs a{f, dout, dq, dk, dv, workspace};
-    return status(swa_tc_supported(d, dtype) ? swa_backward_tc(a, st) : swa_backward_simt(a, st));
+    cudaError_t e = swa_tc_supported(d, dtype) ? swa_backward_tc(a, st) : swa_backward_simt(a, st);
+    if (e == cudaSuccess && (S == 1 || (window == 1 && sinks == 0))) {
+        // every query sees one key, at weight 1 whatever the score: the
+        // gradients are zero, not the rounding of dP - delta
+        e = cudaMemsetAsync(dq, 0, nq, st);
+        if (e == cudaSuccess) e = cudaMemsetAsync(dk, 0, nk, st);
+    }
+    return status(e);
 }
 
 size_t mesa_swa_step_workspace_size(int B, int Hq, int Hkv, int d, int window, int sinks, mesa_dtype dtype) {

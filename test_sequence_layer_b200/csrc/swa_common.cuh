@@ -14,6 +14,28 @@ __device__ __forceinline__ bool visible(int p, int j, int window, int sinks) {
     return j <= p && (p - j < window || j < sinks);
 }
 
+// The backward's delta = rowsum(dout o out) takes out as rounded to bf16. With a
+// handful of visible keys dP - delta is small against delta, and that rounding
+// would show (twice the error of dS's own rounding at two keys, a half at
+// eight); up to kFewKeys of them delta is summed from the weights instead,
+// sum_j P_j dP_j. Key i of the n that position p sees:
+constexpr int kFewKeys = 8;
+struct FewKeys {
+    int sinks, lo, n, p;
+    __device__ __forceinline__ FewKeys(int p_, int window, int all_sinks) : p(p_) {
+        lo = p - window + 1 > 0 ? p - window + 1 : 0;
+        sinks = all_sinks < lo ? all_sinks : lo;
+        n = sinks + p - lo + 1;
+    }
+    __device__ __forceinline__ int key(int i) const {
+        const int j = lo + i - sinks;
+        return i < sinks ? i : j < p ? j : p;          // past the last: some key that exists
+    }
+};
+__host__ __forceinline__ bool few_keys(int window, int sinks, int S) {
+    return (window + sinks < S ? window + sinks : S) <= kFewKeys;
+}
+
 // the n lowest bits of a word
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 

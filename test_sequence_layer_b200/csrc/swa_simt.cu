@@ -189,6 +189,33 @@ __global__ void swa_delta_kernel(const T* __restrict__ out, const T* __restrict_
     if ((threadIdx.x & 31) == 0) delta[r] = s;
 }
 
+// the same from the weights, for rows of few keys
+__global__ void swa_delta_few_kernel(SwaArgs a, const __nv_bfloat16* __restrict__ dout, size_t rows, float* delta) {
+    using bf = __nv_bfloat16;
+    const size_t r = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (r >= rows) return;
+    const size_t head = r / a.T;
+    const size_t kv = head / (a.Hq / a.Hkv) * a.S * a.d;
+    const swa::FewKeys keys(a.S - a.T + (int)(r % a.T), a.window, a.sinks);
+    const float lse = a.lse[r];
+    float s = 0.f;
+    for (int i = 0; i < keys.n; ++i) {
+        const size_t j = kv + (size_t)keys.key(i) * a.d;
+        float qk = 0.f, dv = 0.f;
+        for (int c = threadIdx.x & 31; c < a.d; c += 32) {
+            qk = fmaf(ld_in(static_cast<const bf*>(a.q), r * a.d + c), ld_in(static_cast<const bf*>(a.k), j + c), qk);
+            dv = fmaf(ld_in(dout, r * a.d + c), ld_in(static_cast<const bf*>(a.v), j + c), dv);
+        }
+#pragma unroll
+        for (int x = 16; x; x >>= 1) {
+            qk += __shfl_xor_sync(~0u, qk, x);
+            dv += __shfl_xor_sync(~0u, dv, x);
+        }
+        s = fmaf(expf(qk * a.scale - lse), dv, s);
+    }
+    if ((threadIdx.x & 31) == 0) delta[r] = s;
+}
+
 // P and dS of one 64 x 64 tile pair into shared memory (rows: queries)
 template <int D>
 __device__ __forceinline__ void grad_scores(const SwaArgs& p, const float* sQ, const float* sK, const float* sDo,
@@ -443,6 +470,8 @@ cudaError_t swa_delta(const SwaArgs& a, const void* dout, float* delta, cudaStre
     const unsigned grid = (unsigned)((rows + 7) / 8);
     if (a.dtype == MESA_F32)
         swa_delta_kernel<float><<<grid, 256, 0, st>>>((const float*)a.out, (const float*)dout, rows, a.d, delta);
+    else if (swa::few_keys(a.window, a.sinks, a.S))
+        swa_delta_few_kernel<<<grid, 256, 0, st>>>(a, (const __nv_bfloat16*)dout, rows, delta);
     else
         swa_delta_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>((const __nv_bfloat16*)a.out, (const __nv_bfloat16*)dout,
                                                               rows, a.d, delta);

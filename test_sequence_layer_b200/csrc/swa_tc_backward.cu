@@ -41,12 +41,6 @@ struct BwdParams {
 };
 
 // ---- (lse log2 e, delta) per query ----
-// delta = rowsum(dout o out) takes out as rounded to bf16. With a handful of
-// visible keys dP - delta is small against delta, and that rounding would show
-// (twice the error of dS's own rounding at two keys, a half at eight); up to
-// kFewKeys of them delta is summed from the weights instead, sum_j P_j dP_j.
-constexpr int kFewKeys = 8;
-
 __device__ __forceinline__ float dot8(const uint4& x, const uint4& y) {
     const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
     float s = 0.f;
@@ -77,17 +71,15 @@ __global__ void swa_stats_kernel(SwaArgs a, const __nv_bfloat16* __restrict__ do
     if (FEW) {
         const size_t kv = (size_t)(blockIdx.y / (a.Hq / a.Hkv)) * a.S * D;
         const uint4 q = reinterpret_cast<const uint4*>(static_cast<const bf*>(a.q) + src * D)[piece];
-        const int p = a.S - a.T + (in ? row : 0), lo = max(0, p - a.window + 1);
+        const swa::FewKeys keys(a.S - a.T + (in ? row : 0), a.window, a.sinks);
         delta = 0.f;
-        // every lane of a warp runs kFewKeys steps: step i is sink i, then the window's keys
-        const int sinks = min(a.sinks, lo), n = sinks + p - lo + 1;
 #pragma unroll
-        for (int i = 0; i < kFewKeys; ++i) {
-            const int j = i < sinks ? i : min(lo + i - sinks, p);
+        for (int i = 0; i < swa::kFewKeys; ++i) {      // every lane of a warp runs all steps
+            const int j = keys.key(i);
             const uint4 k = reinterpret_cast<const uint4*>(static_cast<const bf*>(a.k) + kv + (size_t)j * D)[piece];
             const uint4 v = reinterpret_cast<const uint4*>(static_cast<const bf*>(a.v) + kv + (size_t)j * D)[piece];
             const float w = swa::ex2(fmaf(sum(dot8(q, k)), a.scale * swa::kLog2e, -lse2)), dp = sum(dot8(g, v));
-            if (i < n) delta = fmaf(w, dp, delta);
+            if (i < keys.n) delta = fmaf(w, dp, delta);
         }
     } else {
         delta = sum(dot8(reinterpret_cast<const uint4*>(static_cast<const bf*>(a.out) + src * D)[piece], g));
@@ -546,7 +538,7 @@ cudaError_t launch(const SwaBackwardArgs& b, cudaStream_t st) {
     const int rows = 256 / (D / 8);
     const dim3 grid((f.tpad + rows - 1) / rows, a.B * a.Hq);
     const __nv_bfloat16* dout = static_cast<const __nv_bfloat16*>(b.dout);
-    if (a.window + a.sinks <= kFewKeys) swa_stats_kernel<D, true><<<grid, 256, 0, st>>>(a, dout, f.tpad, stats);
+    if (swa::few_keys(a.window, a.sinks, a.S)) swa_stats_kernel<D, true><<<grid, 256, 0, st>>>(a, dout, f.tpad, stats);
     else swa_stats_kernel<D, false><<<grid, 256, 0, st>>>(a, dout, f.tpad, stats);
     const int kt = (a.S + kTile - 1) / kTile;
     swa_tc_dkv_kernel<D><<<dim3(kt - 1 + f.chunks, a.B * a.Hkv), kThreads, DkvSmem<D>::bytes, st>>>(q64, do64, mk, mv, f);

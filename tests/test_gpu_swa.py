@@ -351,15 +351,27 @@ def test_step_refusals(mesa):
     assert e.value.status == 1
 
 
-@pytest.mark.parametrize("window,sinks", [(1, 1), (2, 0), (3, 0), (2, 2), (7, 1), (9, 0)])
-@pytest.mark.parametrize("d", [64, 128])
-def test_few_keys_keep_their_gradients(mesa, d, window, sinks):
+@pytest.mark.parametrize("T,S,window,sinks", [(400, 460, 1, 1), (400, 460, 2, 0), (400, 460, 3, 0), (400, 460, 2, 2),
+                                              (400, 460, 7, 1), (400, 460, 9, 0), (3, 3, 50, 100), (6, 8, 8, 128)])
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+def test_few_keys_keep_their_gradients(mesa, d, T, S, window, sinks):
     """With two or three keys dP - delta cancels: the gradients' error as a whole
     stays within the roundings of P, dS and the result to bf16, 3 x 2^-9 in the
     root mean square (a half step is 2^-9 on average over a binade at most)."""
-    q, k, v, do = inputs(1, 4, 2, 400, 460, d, "bf16", seed=31)
+    q, k, v, do = inputs(1, 4, 2, T, S, d, "bf16", seed=31)
     out, lse = mesa.swa_forward(q, k, v, window=window, sinks=sinks, return_lse=True)
     want = ref.swa(q, k, v, window, sinks, matrix=True, dout=do)
     for n, g in zip(("dq", "dk", "dv"), mesa.swa_backward(q, k, v, out, lse, do, window=window, sinks=sinks)):
         err = (g.double() - want[n][0]).norm() / want[n][0].norm()
         assert float(err) <= 3 * 2.0 ** -9, (n, float(err))
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 32), ("bf16", 16), ("bf16", 64), ("bf16", 128)])
+def test_one_visible_key_has_no_score_gradient(mesa, dtype, d):
+    for T, S, window, sinks in ((130, 200, 1, 0), (1, 1, 9, 4)):
+        q, k, v, do = inputs(2, 4, 2, T, S, d, dtype, seed=32)
+        out, lse = mesa.swa_forward(q, k, v, window=window, sinks=sinks, return_lse=True)
+        dq, dk, dv = mesa.swa_backward(q, k, v, out, lse, do, window=window, sinks=sinks)
+        assert torch.count_nonzero(dq) == 0 and torch.count_nonzero(dk) == 0
+        want = ref.swa(q, k, v, window, sinks, matrix=ref.matrix_path(q.dtype, d), dout=do)
+        ref.check(dv, *want["dv"], "dv")
