@@ -13,8 +13,8 @@
 //            and ragged batches leave none idle.
 //
 // 64 sequences, 16 over 4 heads, 4100 slots, d = 128: 92 us by shares, 5.1 TB/s
-// (0.79 of the measured copy rate), 102 by clusters. Below 8 MB of cache the
-// cluster is faster: its one launch against two.
+// (0.79 of the measured copy rate), 102 by clusters. Up to 8 MB of cache the
+// cluster is as fast or faster: its one launch against two.
 //
 // The new token's rows are read from the arguments, not from the cache: their
 // slot is written by one CTA while others run, and nobody reads it.
@@ -630,7 +630,9 @@ cudaError_t launch_cluster(F* kernel, const SwaStepArgs& a, int hgroups, int slo
     return cudaLaunchKernelEx(&cfg, kernel, a, splits);
 }
 
-// The second launch costs about 2 us: worth it from some MB of cache on.
+// Both launches against the cluster's one, events around a call: 15.4 us against
+// 13.2 at 4 MB (8 heads of 1028 slots), 15.4 against 12.4 at 7.9 MB (32 heads of
+// 504), 15.3 against 16.1 at 8.0 MB (8 heads of 2048), 20 against 30 at 16.8 MB.
 bool use_stream(const SwaStepArgs& a) {
     if (a.dtype != MESA_BF16 || (a.d != 64 && a.d != 128)) return false;
     return (long long)a.B * a.Hkv * ((long long)a.sinks + a.window) * a.d * 4 >= (8LL << 20);
