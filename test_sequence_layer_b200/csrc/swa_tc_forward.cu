@@ -380,9 +380,13 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 ++n;
             }
             // ---- output ----
+            float l = 1.f;
+            if (q.live) l = exchange(l2.x + l2.y, [](float u, float v) { return u + v; });
+            // A tile past the last query waits as well: without it its warps would
+            // arrive on o_free items ahead and complete phases in the others' place.
+            if (ok) ok = swa::wait_bar(o_full, k & 1);
             if (q.live) {
-                const float l = exchange(l2.x + l2.y, [](float u, float v) { return u + v; }), inv = 1.f / l;
-                if (ok) ok = swa::wait_bar(o_full, k & 1);
+                const float inv = 1.f / l;
                 tc_fence_after();
                 const int tq = q.t0 + row;
                 const bool in = tq < a.T && ok;

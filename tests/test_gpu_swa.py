@@ -375,3 +375,34 @@ def test_one_visible_key_has_no_score_gradient(mesa, dtype, d):
         assert torch.count_nonzero(dq) == 0 and torch.count_nonzero(dk) == 0
         want = ref.swa(q, k, v, window, sinks, matrix=ref.matrix_path(q.dtype, d), dout=do)
         ref.check(dv, *want["dv"], "dv")
+
+
+# (B, Hq, Hkv, T, window, sinks): every SM's CTA walks several pairs of query tiles. Heads that
+# share no keys in pairs with an odd number of 128-row tiles: the pair's second tile is empty.
+WALKS = [
+    (32, 16, 16, 100, 40, 3),        # one tile a head, 512 pairs, all second tiles empty
+    (30, 10, 10, 300, 70, 2),        # three tiles, two pairs a head: every second one half empty
+    (6, 16, 16, 800, 150, 4),        # seven tiles
+    (34, 9, 3, 129, 64, 0),          # groups of three, both tiles live
+    (16, 40, 20, 200, 90, 1),        # pairs of heads
+    (150, 3, 1, 1, 5, 0),            # one query a head
+]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("case", WALKS, ids=lambda c: "-".join(map(str, c)))
+def test_forward_walks_several_pairs(mesa, case, d):
+    B, Hq, Hkv, T, window, sinks = case
+    S = T + 30 if T < 200 else T
+    pairs = B * Hq // 2 * -(-T // 128) if (Hq // Hkv) % 2 == 0 else B * Hq * -(-T // 256)
+    assert pairs > 2 * 148
+    q, k, v, _ = inputs(B, Hq, Hkv, T, S, d, "bf16", seed=41)
+    assert mesa.get_error() == 0
+    out, lse = mesa.swa_forward(q, k, v, window=window, sinks=sinks, return_lse=True)
+    assert mesa.get_error() == 0                                      # no wait gave up
+    for b in range(0, B, 2):
+        at = slice(b, b + 2)
+        want = ref.swa(q[at], k[at], v[at], window, sinks, matrix=True)
+        ref.check(out[at], *want["out"], f"out of sequences {b}, {b + 1}")
+        ref.check(lse[at], *want["lse"], f"lse of sequences {b}, {b + 1}")
+    assert torch.equal(out, mesa.swa_forward(q, k, v, window=window, sinks=sinks))
