@@ -247,6 +247,12 @@ template <int NW_, int SEG_, int NS_> struct Shape {
 
 enum Load { kTensor, kAsync4, kPlain };
 
+// A cluster's last round has tiles past the end (forward) or below 0
+// (backward): their tokens are not in memory.
+__host__ __device__ constexpr bool token_exists(int t, int T) { return t >= 0 && t < T; }
+static_assert(!token_exists(-1, 5) && !token_exists(-64, 5) && token_exists(0, 5) && token_exists(4, 5) && !token_exists(5, 5),
+              "reads outside a sequence");
+
 // NT input tensors of a CTA's channels, NS tiles ahead in shared memory.
 // Words of 4 bytes, [stage][tensor][token][lane]: a lane's VEC channels.
 template <typename T, int VEC, int NT, int LOAD, typename S> struct Stager {
@@ -300,7 +306,7 @@ template <typename T, int VEC, int NT, int LOAD, typename S> struct Stager {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         if (LOAD == kPlain) {
             const int t = tile * kTile + warp * kSeg + s;
-            return live && t < T_ ? R::load(src[i], (size_t)t * D) : R::zero();
+            return live && token_exists(t, T_) ? R::load(src[i], (size_t)t * D) : R::zero();
         }
         const uint32_t w = buf[(((round % NS) * NT + i) * kTile + warp * kSeg + s) * 32 + lane];
         return *reinterpret_cast<const typename R::Raw*>(&w);

@@ -249,3 +249,23 @@ def test_refusals(mesa):
     with pytest.raises(mesa.MesaError) as e:
         mesa.lru_forward(x, ga, gx, lam, y=x)
     assert e.value.status == 1
+
+
+# (B, T, D, shift): rows that only single-element loads can take, and numbers of 64-token tiles
+# that leave a cluster's last round with tiles that do not exist
+PLAIN = [(1, 130, 17, 0), (1, 300, 33, 0), (1, 1900, 33, 0), (1, 1900, 1003, 0), (1, 6000, 31, 0), (2, 130, 34, 1),
+         (3, 321, 64, 1), (1, 2000, 130, 1)]
+
+
+@pytest.mark.parametrize("B,T,D,shift", PLAIN)
+def test_rows_of_single_elements(mesa, B, T, D, shift):
+    x, ga, gx, lam, dy, h0, dh = inputs(B, T, D, "bf16", seed=T + D, shift=shift)
+    y, hT, saved = mesa.lru_forward(x, ga, gx, lam, h0=h0, return_state=True, return_saved=True)
+    want, wT, ey, eT = ref.lru(x, ga, gx, lam, h0)
+    ref.check(y, want, ey, "y")
+    ref.check(hT, wT, eT, "h_T")
+    got = mesa.lru_backward(x, ga, gx, lam, dy, saved=saved, dh_T=dh)
+    want, bound = ref.lru_grads(x, ga, gx, lam, h0, dy, dh)
+    for n, o, w, b in zip(("dx", "dgate_a", "dgate_x", "dlam", "dh0"), got, want, bound):
+        ref.check(o, w, b, n)
+    assert mesa.get_error() == 0
