@@ -90,8 +90,8 @@ __global__ void __launch_bounds__(kSimtThreads) swa_step_simt_kernel(SwaStepArgs
         for (int i = rank * kSimtThreads + tid; i < rows * D; i += splits * kSimtThreads) out[i] = to_out<T>(0.f);
         return;
     }
-    const int cap = p.sinks + p.window, own = slot_of(pos, p.window, p.sinks);
-    const int n = pos < cap - 1 ? pos + 1 : cap;
+    const int cap = p.sinks + p.window;
+    const unsigned own = slot_of(pos, p.window, p.sinks), n = pos < cap - 1 ? pos + 1 : cap;
     const T* kin = static_cast<const T*>(p.k) + ((size_t)b * p.Hkv + hk) * D;
     const T* vin = static_cast<const T*>(p.v) + ((size_t)b * p.Hkv + hk) * D;
     T* kc = static_cast<T*>(p.kc) + ((size_t)b * p.Hkv + hk) * cap * D;
@@ -111,11 +111,12 @@ __global__ void __launch_bounds__(kSimtThreads) swa_step_simt_kernel(SwaStepArgs
     for (int r = 0; r < kSimtRows; ++r) o[r] = 0.f;
     if (tid < kSimtRows) part.m[tid] = -INFINITY, part.l[tid] = 0.f;
     __syncthreads();
-    for (int s0 = rank * kSimtThreads; s0 < n; s0 += splits * kSimtThreads) {
+    // unsigned: the last step starts below n < 2^31 and ends above it
+    for (unsigned s0 = rank * kSimtThreads; s0 < n; s0 += splits * kSimtThreads) {
         float s[kSimtRows];
 #pragma unroll
         for (int r = 0; r < kSimtRows; ++r) s[r] = 0.f;
-        const int slot = s0 + tid;
+        const unsigned slot = s0 + tid;
         if (slot < n) {
             const T* kr = slot == own ? kin : kc + (size_t)slot * D;
 #pragma unroll 4
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(kSimtThreads) swa_step_simt_kernel(SwaStepArgs
             }
         }
         __syncthreads();
-        const int c = tid % D, first = tid / D, last = min(kSimtThreads, n - s0);
+        const int c = tid % D, first = tid / D, last = min((unsigned)kSimtThreads, n - s0);
 #pragma unroll
         for (int r = 0; r < kSimtRows; ++r) o[r] *= keep[r];
         for (int i = first; i < last; i += kParts) {

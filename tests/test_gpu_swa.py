@@ -406,3 +406,30 @@ def test_forward_walks_several_pairs(mesa, case, d):
         ref.check(out[at], *want["out"], f"out of sequences {b}, {b + 1}")
         ref.check(lse[at], *want["lse"], f"lse of sequences {b}, {b + 1}")
     assert torch.equal(out, mesa.swa_forward(q, k, v, window=window, sinks=sinks))
+
+
+def test_cache_of_the_most_slots(mesa):
+    """sinks + window = 2^31 - 1: slot numbers pass 31 bits within a step of the last CTA."""
+    d, sinks = 16, 4
+    cap = 2 ** 31 - 1
+    window = cap - sinks
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 2 * cap * d * 2 + (2 << 30):
+        pytest.skip("needs 140 GB of device memory")
+    kc, vc = (torch.zeros(1, 1, cap, d, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    # scores of 0 but for a few slots of score 32, those in the last steps among them
+    at = torch.tensor([0, 7, 2 ** 30 + 1, cap - 2049, cap - 2047, cap - 129, cap - 128, cap - 2, cap - 1], device="cuda")
+    g = torch.Generator().manual_seed(43)
+    kc[0, 0, at] = 8.0
+    vc[0, 0, at] = torch.randn(len(at), d, generator=g).cuda().bfloat16()
+    q, k = torch.ones(1, 1, d, device="cuda").bfloat16(), torch.zeros(1, 1, d, device="cuda").bfloat16()
+    v = k.clone()
+    pos = torch.tensor([cap], dtype=torch.int32, device="cuda")            # slot 4; every slot is in use
+    out = mesa.swa_step(q, k, v, kc, vc, pos, window=window, sinks=sinks)
+    want = vc[0, 0, at].double().sum(0) / (len(at) + (cap - len(at)) * 2.718281828459045 ** -32)
+    # exponents of 46 in log2 units err by 46 U; the 2^31 weights of e^-32, lost or not in a sum of nine, are 2.7e-5 < 2^-15
+    bound = 2.0 ** -14 * vc[0, 0, at].double().abs().sum(0)
+    ref.check(out[0, 0], want, bound, "out")
+    assert mesa.get_error() == 0
+    del kc, vc
+    torch.cuda.empty_cache()
