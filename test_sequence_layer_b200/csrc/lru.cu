@@ -349,8 +349,17 @@ template <int VEC> struct Exchange {
     }
 };
 
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 
 struct Where {
@@ -406,6 +415,9 @@ __device__ __forceinline__ bool forward_walk(const LruArgs& p, const Where& w, i
     W carry;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) carry.v[e] = w.live && p.h0 ? p.h0[(size_t)w.b * p.D + w.c0 + e] : 0.f;
+    // h_T in the place of h0 is written only when every CTA has read h0
+    const bool in_place = ncta > 1 && p.h0 && p.h0 == p.hT;
+    if (in_place) cluster_arrive();
     for (int j = 0; j < w.rounds; ++j) {
         const int tile = j * ncta + w.rank;
         const int t0 = tile * S::kTokens + warp * kSeg;
@@ -485,6 +497,7 @@ __device__ __forceinline__ bool forward_walk(const LruArgs& p, const Where& w, i
             }
         }
     }
+    if (in_place) cluster_wait();
     if (p.hT && w.live && w.rank == 0 && warp == 0) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) p.hT[(size_t)w.b * p.D + w.c0 + e] = carry.v[e];

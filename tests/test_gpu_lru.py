@@ -269,3 +269,18 @@ def test_rows_of_single_elements(mesa, B, T, D, shift):
     for n, o, w, b in zip(("dx", "dgate_a", "dgate_x", "dlam", "dh0"), got, want, bound):
         ref.check(o, w, b, n)
     assert mesa.get_error() == 0
+
+
+@pytest.mark.parametrize("B,T,D", [(1, 1, 32), (1, 130, 64), (1, 256, 32), (2, 300, 130), (1, 2049, 64), (1, 5000, 33),
+                                   (40, 257, 256)])
+def test_state_in_place(mesa, B, T, D):
+    """h_T may be h0 itself, also where several CTAs share a sequence and all read h0."""
+    x, ga, gx, lam, _, h0, _ = inputs(B, T, D, "bf16", seed=T)
+    want, wT = mesa.lru_forward(x, ga, gx, lam, h0=h0, return_state=True)
+    lib, y, h = mesa._load(), torch.empty_like(x), torch.empty_like(h0)
+    stream = torch.cuda.current_stream().cuda_stream
+    for _ in range(20):
+        h.copy_(h0)
+        assert lib.mesa_lru_forward(x.data_ptr(), ga.data_ptr(), gx.data_ptr(), lam.data_ptr(), B, T, D, 1, h.data_ptr(),
+                                    y.data_ptr(), h.data_ptr(), None, stream) == 0
+        assert torch.equal(h, wT) and torch.equal(y, want)
