@@ -162,6 +162,20 @@ mesa_status mesa_swa_cache_fill(const void* k, const void* v, void* k_cache, voi
                                 int B, int Hkv, int S, int d, int window, int sinks, int start, mesa_dtype dtype,
                                 void* stream);
 
+#ifdef MESA_DEBUG
+/*
+ * Debug builds only: fault injection for the failure-detection tests. In the
+ * next `launches` launches of this file's kernels with bounded waits (the
+ * recurrence's forward and backward, the tensor-core attention kernels) one
+ * signal per CTA never comes: a tile copy of a cluster's first CTA, or the
+ * completion of the first scores. The waits on it run out (about one second of
+ * clock cycles each), the kernel records a timeout in the error word, lets its
+ * copies and products drain and returns; its outputs are then undefined.
+ * Returns MESA_ERR_INVALID_ARG for launches < 0.
+ */
+mesa_status mesa_debug_lose_signal(int launches);
+#endif
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,6 +1,7 @@
 """Builds libmesa_b200.so in-tree with nvcc for sm_100a, and its MESA_DEBUG
 variant libmesa_b200_debug.so (the same library plus the fault-injection
-entry point mesa_debug_skip_commit, used by the failure-detection tests).
+entry points mesa_debug_skip_commit and mesa_debug_lose_signal, used by the
+failure-detection tests).
 
 Usage: python -m test_sequence_layer_b200.build [--force] [--verbose-ptxas] [--debug]
 """

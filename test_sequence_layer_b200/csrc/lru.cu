@@ -266,17 +266,25 @@ template <typename T, int VEC, int NT, int LOAD, typename S> struct Stager {
     uint64_t* full;                             // [NS]
     int T_, D, c_cta, b;
     bool live;
+#ifdef MESA_DEBUG
+    bool lose = false;
+#endif
 
-    // a round up to NS ahead; call by all threads, tile < 0 or past the end: nothing to load
-    __device__ __forceinline__ void issue(int round, int tile, int tiles) {
+    // A round up to NS ahead; call by all threads, tile < 0 or past the end: nothing to load.
+    // After a wait that was given up thread 0 issues no more: the barrier's phase is open.
+    __device__ __forceinline__ void issue(int round, int tile, int tiles, bool ok) {
         if (tile < 0 || tile >= tiles) return;
         const int st = round % NS, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         if (LOAD == kTensor) {
-            if (threadIdx.x == 0) {
+            if (threadIdx.x == 0 && ok) {
                 tc::mbar_arrive_expect_tx(&full[st], kStageBytes);
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
+                for (int i = 0; i < NT; ++i) {
+#ifdef MESA_DEBUG
+                    if (lose && round == 0 && i == 0) continue;       // fault injection: this copy never lands
+#endif
                     swa::tma_load(buf + (st * NT + i) * kTile * 32, maps[i], c_cta, tile * kTile, b, &full[st]);
+                }
             }
         } else if (LOAD == kAsync4) {
             const int t0 = tile * kTile + warp * kSeg;
@@ -323,11 +331,11 @@ template <int VEC> struct Exchange {
     W2<VEC>* peer;                              // [2][ncta][32]
     uint64_t* bar;                              // [2]
     int ncta, rank;
-    // this CTA's map to every CTA of the cluster, itself included
+    // This CTA's map to every CTA of the cluster, itself included. Lanes that
+    // gave up a wait send no more, so that the others give up as well.
     __device__ __forceinline__ void send(int round, const W2<VEC>& m) {
         const int par = round & 1, lane = threadIdx.x & 31;
         if (lane == 0) tc::mbar_arrive_expect_tx(&bar[par], ncta * 32 * (int)sizeof(W2<VEC>));
-        __syncwarp();
         const uint32_t b0 = tc::smem_addr(&bar[par]), a0 = tc::smem_addr(&peer[(par * ncta + rank) * 32 + lane]);
         for (int r = 0; r < ncta; ++r) {
             uint32_t rb, ra;
@@ -360,6 +368,19 @@ __device__ __forceinline__ void cluster_wait() {
 __device__ __forceinline__ void cluster_sync() {
     cluster_arrive();
     cluster_wait();
+}
+
+// End of a kernel. A CTA that gave up a wait says so, and leaves when nothing
+// can write to its shared memory any more. Its copies have had that wait's second
+// to land, since the last was issued before it began; the other CTAs, which may
+// still send it their maps, are done (threads that have returned count as
+// arrived). A CTA that met all its waits has received everything.
+__device__ __forceinline__ void leave(bool ok, int ncta, unsigned* err) {
+    if (!ok) {
+        record_error(err, kErrTimeout);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+    if (ncta > 1 && __syncthreads_or(!ok)) cluster_sync();
 }
 
 struct Where {
@@ -444,7 +465,7 @@ __device__ __forceinline__ bool forward_walk(const LruArgs& p, const Where& w, i
         }
         sh.run[warp][lane] = {A, Hl};
         __syncthreads();
-        in.issue(j, tile + S::NS * ncta, w.tiles);   // every thread has read the stage
+        in.issue(j, tile + S::NS * ncta, w.tiles, ok);   // every thread has read the stage
         if (warp == 0) {
             W c = carry;
             if (ncta > 1) {
@@ -454,8 +475,10 @@ __device__ __forceinline__ bool forward_walk(const LruArgs& p, const Where& w, i
                     const W2<VEC> g = sh.run[u][lane];
                     m = {W::mul(g.a, m.a), W::fma(g.a, m.b, g.b)};
                 }
-                ex.send(j, m);
-                if (ok) ok = ex.wait(j);
+                if (ok) {
+                    ex.send(j, m);
+                    ok = ex.wait(j);
+                }
                 W mine = c;
                 for (int r = 0; r < ncta; ++r) {
                     if (r == w.rank) mine = c;
@@ -516,18 +539,21 @@ lru_forward_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
     St in{{&mx, &ma, &mg},
           {static_cast<const T*>(p.x) + w.base, static_cast<const T*>(p.ga) + w.base, static_cast<const T*>(p.gx) + w.base},
           reinterpret_cast<uint32_t*>(smem), sh.bars, p.T, p.D, w.c_cta, w.b, w.live};
+#ifdef MESA_DEBUG
+    in.lose = p.lose && w.rank == 0;
+#endif
     Exchange<VEC> ex{reinterpret_cast<W2<VEC>*>(smem + St::kBytes), sh.bars + 2, ncta, w.rank};
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) tc::mbar_init(&sh.bars[i], 1);
         tc::fence_mbar_init();
     }
     if (ncta > 1) cluster_sync(); else __syncthreads();
-    for (int i = 0; i < S::NS; ++i) in.issue(i, w.rank + i * ncta, w.tiles);
+    for (int i = 0; i < S::NS; ++i) in.issue(i, w.rank + i * ncta, w.tiles, true);
     bool small;
     const V<VEC> k = channel_k<VEC>(p, w, small);
     const bool ok = small ? forward_walk<T, VEC, LOAD, S, true>(p, w, ncta, k, in, ex, sh)
                           : forward_walk<T, VEC, LOAD, S, false>(p, w, ncta, k, in, ex, sh);
-    if (!ok) record_error(err, kErrTimeout);
+    leave(ok, ncta, err);
 }
 
 // ---- backward ----
@@ -600,7 +626,7 @@ __device__ __forceinline__ bool backward_walk(const LruBackwardArgs& q, const Wh
         sh.run[warp][lane] = {A, Hl};
         sh.runc[warp][lane] = Cl;
         __syncthreads();
-        in.issue(j, tile - S::NS * ncta, w.tiles);
+        in.issue(j, tile - S::NS * ncta, w.tiles, ok);
         if (warp == 0) {
             W c = carry;
             if (ncta > 1) {
@@ -610,8 +636,10 @@ __device__ __forceinline__ bool backward_walk(const LruBackwardArgs& q, const Wh
                     const W ra = sh.run[u][lane].a;
                     m = {W::mul(ra, m.a), W::fma(ra, m.b, sh.runc[u][lane])};
                 }
-                ex.send(j, m);
-                if (ok) ok = ex.wait(j);
+                if (ok) {
+                    ex.send(j, m);
+                    ok = ex.wait(j);
+                }
                 W mine = c;
                 for (int t = 0; t < ncta; ++t) {
                     if (t == w.rank) mine = c;
@@ -699,18 +727,21 @@ lru_backward_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
           {static_cast<const T*>(p.x) + w.base, static_cast<const T*>(p.ga) + w.base, static_cast<const T*>(p.gx) + w.base,
            static_cast<const T*>(q.dy) + w.base},
           reinterpret_cast<uint32_t*>(smem), sh.bars, p.T, p.D, w.c_cta, w.b, w.live};
+#ifdef MESA_DEBUG
+    in.lose = p.lose && w.rank == 0;
+#endif
     Exchange<VEC> ex{reinterpret_cast<W2<VEC>*>(smem + St::kBytes), sh.bars + 2, ncta, w.rank};
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) tc::mbar_init(&sh.bars[i], 1);
         tc::fence_mbar_init();
     }
     if (ncta > 1) cluster_sync(); else __syncthreads();
-    for (int i = 0; i < S::NS; ++i) in.issue(i, w.tiles - 1 - w.rank - i * ncta, w.tiles);
+    for (int i = 0; i < S::NS; ++i) in.issue(i, w.tiles - 1 - w.rank - i * ncta, w.tiles, true);
     bool small;
     const V<VEC> k = channel_k<VEC>(p, w, small);
     const bool ok = small ? backward_walk<T, VEC, LOAD, S, true>(q, w, ncta, k, in, ex, sh)
                           : backward_walk<T, VEC, LOAD, S, false>(q, w, ncta, k, in, ex, sh);
-    if (!ok) record_error(err, kErrTimeout);
+    leave(ok, ncta, err);
 }
 
 // dlambda = sigmoid(lambda) / softplus(lambda) * sum over rows of partial
@@ -862,8 +893,12 @@ size_t lru_backward_rows(int B, int T) {
     return (size_t)B * (t < 1 ? 1 : t < kLruMaxCluster ? t : kLruMaxCluster);
 }
 
-cudaError_t lru_forward(const LruArgs& a, cudaStream_t st) {
+cudaError_t lru_forward(const LruArgs& args, cudaStream_t st) {
     LaunchTimer lt(kKindLru, st);
+    LruArgs a = args;
+#ifdef MESA_DEBUG
+    a.lose = debug_lose_signal();
+#endif
     unsigned* err = error_word_ptr();
     if (!err) return cudaErrorUnknown;
     using bf = __nv_bfloat16;
@@ -873,9 +908,13 @@ cudaError_t lru_forward(const LruArgs& a, cudaStream_t st) {
     return pair_ok(a.D, {a.x, a.ga, a.gx, a.y}) ? forward<bf, 2, kAsync4>(a, err, st) : forward<bf, 1, kPlain>(a, err, st);
 }
 
-cudaError_t lru_backward(const LruBackwardArgs& q, cudaStream_t st) {
+cudaError_t lru_backward(const LruBackwardArgs& args, cudaStream_t st) {
     LaunchTimer lt(kKindLruBwd, st);
+    LruBackwardArgs q = args;
     const LruArgs& a = q.f;
+#ifdef MESA_DEBUG
+    q.f.lose = debug_lose_signal();
+#endif
     unsigned* err = error_word_ptr();
     if (!err) return cudaErrorUnknown;
     using bf = __nv_bfloat16;

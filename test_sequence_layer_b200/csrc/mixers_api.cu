@@ -74,7 +74,15 @@ mesa_status step_shape(int B, int Hq, int Hkv, int d, int window, int sinks, flo
     return (long long)sinks + window > 0x7fffffffLL ? MESA_ERR_UNSUPPORTED : MESA_OK;
 }
 
+#ifdef MESA_DEBUG
+int g_lose_signals = 0;
+#endif
+
 }  // namespace
+
+#ifdef MESA_DEBUG
+int mesa::debug_lose_signal() { return g_lose_signals > 0 ? g_lose_signals--, 1 : 0; }
+#endif
 
 extern "C" {
 
@@ -256,5 +264,13 @@ mesa_status mesa_swa_cache_fill(const void* k, const void* v, void* k_cache, voi
     return status(swa_cache_fill(k, v, k_cache, v_cache, lens, B, Hkv, S, d, window, sinks, start, dtype,
                                  static_cast<cudaStream_t>(stream)));
 }
+
+#ifdef MESA_DEBUG
+mesa_status mesa_debug_lose_signal(int launches) {
+    if (launches < 0) return MESA_ERR_INVALID_ARG;
+    g_lose_signals = launches;
+    return MESA_OK;
+}
+#endif
 
 }  // extern "C"

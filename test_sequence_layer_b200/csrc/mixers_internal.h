@@ -13,6 +13,10 @@ namespace mesa {
 constexpr int kLruSave = 64;       // tokens between saved states
 constexpr int kLruMaxCluster = 16;  // CTAs that share one sequence's time axis
 
+#ifdef MESA_DEBUG
+int debug_lose_signal();           // 1 if the launch at hand is to lose a signal
+#endif
+
 struct LruArgs {
     const void* x;
     const void* ga;
@@ -24,6 +28,9 @@ struct LruArgs {
     void* y;                // nullptr: the states only
     float* hT;
     float* saved;
+#ifdef MESA_DEBUG
+    int lose = 0;
+#endif
 };
 struct LruBackwardArgs {
     LruArgs f;              // f.saved holds the states (read)

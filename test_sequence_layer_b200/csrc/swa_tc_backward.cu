@@ -44,6 +44,9 @@ struct BwdParams {
     float* parts;                                    // [B Hkv][chunks][2][128][D]
     int chunks, chunk_len;                           // of the sink tile's queries
     unsigned* err;
+#ifdef MESA_DEBUG
+    int lose;
+#endif
 };
 
 // ---- (lse log2 e, delta) per query ----
@@ -195,19 +198,26 @@ swa_tc_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 swa::tma_load(smem + L::oQ + c * 16384, &mq, c * 64, t0, head, bar_q);
                 swa::tma_load(smem + L::oDo + c * 16384, &mdo, c * 64, t0, head, bar_q);
             }
+            int nk = 0, nv = 0;                              // tiles whose copies were issued
             for (int n = 0; n < kt.n && ok; ++n) {
                 const int sk = n % 3, sv = n & 1, j0 = kt.tile(n) * kTile;
                 ok = swa::wait_bar(&k_empty[sk], ((n / 3) & 1) ^ 1);
                 if (!ok) break;
+                nk = n + 1;
                 mbar_arrive_expect_tx(&k_full[sk], L::kBytes);
                 for (int c = 0; c < D / 64; ++c)
                     swa::tma_load(smem + L::oK + sk * L::kBytes + c * 16384, &mk, c * 64, j0, hkv, &k_full[sk]);
                 ok = swa::wait_bar(&v_empty[sv], ((n >> 1) & 1) ^ 1);
                 if (!ok) break;
+                nv = n + 1;
                 mbar_arrive_expect_tx(&v_full[sv], L::kBytes);
                 for (int c = 0; c < D / 64; ++c)
                     swa::tma_load(smem + L::oV + sv * L::kBytes + c * 16384, &mv, c * 64, j0, hkv, &v_full[sv]);
             }
+            // leave only when every copy has landed
+            bool landed = mbar_wait(bar_q, 0);
+            for (int n = max(0, nk - 3); n < nk && landed; ++n) landed = mbar_wait(&k_full[n % 3], (n / 3) & 1);
+            for (int n = max(0, nv - 2); n < nv && landed; ++n) landed = mbar_wait(&v_full[n & 1], (n >> 1) & 1);
         }
     } else if (warp == 9) {
         if (lane == 0) {
@@ -230,6 +240,9 @@ swa_tc_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             auto dprobs = [&](int n) {
                 if (!swa::wait_bar(&v_full[n & 1], (n >> 1) & 1)) return false;
                 product(tDp, sdo, sv + (n & 1) * L::kBytes);
+#ifdef MESA_DEBUG
+                if (!(f.lose && n == 0))               // fault injection: nothing signals the first
+#endif
                 mma_commit(s_full);
                 mma_commit(&v_empty[n & 1]);
                 return true;
@@ -370,10 +383,12 @@ swa_tc_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 swa::tma_load(smem + L::oK + c * 16384, &mk, c * 64, j0, hkv, bar_k);
                 swa::tma_load(smem + L::oV + c * 16384, &mv, c * 64, j0, hkv, bar_k);
             }
+            int issued = 0;
             for (int n = 0; n < steps && ok; ++n) {
                 const int st = n % L::kStages, head = hkv * G + n / per, t = ta + (n % per) * kSub;
                 ok = swa::wait_bar(&empty[st], ((n / L::kStages) & 1) ^ 1);
                 if (!ok) break;
+                issued = n + 1;
                 mbar_arrive_expect_tx(&full[st], 2 * L::kPiece + kSub * 8);
                 uint8_t* dst = smem + L::oRing + st * 2 * L::kPiece;
                 for (int c = 0; c < D / 64; ++c) {
@@ -382,6 +397,10 @@ swa_tc_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 }
                 bulk_g2s(smem + L::oStat + st * kSub * 8, f.stats + (size_t)head * f.tpad + t, kSub * 8, &full[st]);
             }
+            // leave only when every copy has landed
+            bool landed = mbar_wait(bar_k, 0);
+            for (int n = max(0, issued - L::kStages); n < issued && landed; ++n)
+                landed = mbar_wait(&full[n % L::kStages], (n / L::kStages) & 1);
         }
     } else if (warp == 9) {
         if (lane == 0 && steps > 0) {
@@ -401,6 +420,9 @@ swa_tc_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                     const uint32_t x = (s / 4) * 16384 + (s % 4) * 32, y = (s / 4) * 8192 + (s % 4) * 32;
                     mma_f16(t + 64, sdesc(sv + x, 0, 1024), sdesc(o + y, 0, 1024), idS, s > 0);
                 }
+#ifdef MESA_DEBUG
+                if (!(f.lose && n == 0))               // fault injection: nothing signals the first
+#endif
                 mma_commit(&s_full[n & 1]);
                 return true;
             };
@@ -547,7 +569,13 @@ cudaError_t launch(const SwaBackwardArgs& b, cudaStream_t st) {
     if (swa::few_keys(a.window, a.sinks, a.S)) swa_stats_kernel<D, true><<<grid, 256, 0, st>>>(a, dout, f.tpad, stats);
     else swa_stats_kernel<D, false><<<grid, 256, 0, st>>>(a, dout, f.tpad, stats);
     const int kt = (a.S + kTile - 1) / kTile;
+#ifdef MESA_DEBUG
+    f.lose = debug_lose_signal();
+#endif
     swa_tc_dkv_kernel<D><<<dim3(kt - 1 + f.chunks, a.B * a.Hkv), kThreads, DkvSmem<D>::bytes, st>>>(q64, do64, mk, mv, f);
+#ifdef MESA_DEBUG
+    f.lose = debug_lose_signal();
+#endif
     swa_tc_dq_kernel<D><<<dim3(f.tpad / kTile, a.B * a.Hq), kThreads, DqSmem<D>::bytes, st>>>(q128, do128, mk, mv, f);
     if (f.chunks > 1) {
         const int n = a.S < kTile ? a.S : kTile;

@@ -89,6 +89,9 @@ struct FwdParams {
     int pair_heads;      // 1: the two tiles are heads 2 i, 2 i + 1 of one group; 0: consecutive tiles of one head
     int nx, items;       // pairs along the queries, pairs in all
     unsigned* err;
+#ifdef MESA_DEBUG
+    int lose;
+#endif
 };
 
 // One query tile of an item as every role of the CTA sees it.
@@ -179,6 +182,10 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                     if (++st == L::kStages) st = 0, ph ^= 1;
                 }
             }
+            // leave only when every copy has landed: the last of each stage and of
+            // the query tiles (a parity that was never issued counts as done)
+            bool landed = mbar_wait(bar_q, (k & 1) ^ 1);
+            for (int i = 0; i < L::kStages && landed; ++i) landed = mbar_wait(&full[i], i < st ? ph ^ 1 : ph);
         }
     } else if (warp > kSoftmaxWarps) {
         if (lane == 0) {
@@ -201,6 +208,9 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                     const uint32_t o = ((s / 4) * 16384 + (s % 4) * 32) >> 4;
                     mma_f16(tm + 128 * x, dq + (x * L::kTile >> 4) + o, dk + (stage * L::kPiece >> 4) + o, idS, s > 0);
                 }
+#ifdef MESA_DEBUG
+                if (f.lose && x == 0 && np[0] == 0) return;          // fault injection: nothing signals them
+#endif
                 mma_commit(&s_full[x]);
             };
             auto values = [&](int x, int stage) {
@@ -429,6 +439,9 @@ cudaError_t launch(const SwaArgs& a, cudaStream_t st) {
     const int nx = pair_heads ? tiles : (tiles + 1) / 2, ny = a.B * a.Hq / (pair_heads ? 2 : 1);
     if ((long long)nx * ny > 0x7fffffffLL) return cudaErrorInvalidValue;
     FwdParams f{a, pair_heads, nx, nx * ny, error_word_ptr()};
+#ifdef MESA_DEBUG
+    f.lose = debug_lose_signal();
+#endif
     if (!f.err) return cudaErrorUnknown;
     cudaError_t e = cudaFuncSetAttribute(swa_tc_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes);
     if (e != cudaSuccess) return e;

@@ -66,3 +66,52 @@ def test_bounded_wait_timeout_is_reported_and_context_survives(dlib, oracle_mod)
     assert dlib.mesa_get_error(None) == MESA_OK
     ref, _, _, _ = oracle_mod.forward_cg(xh["q"], xh["k"], xh["v"], xh["gamma"], xh["beta"], xh["lam"], 15)
     assert rel_err(out.cpu().numpy(), ref) <= TOL_BF16
+
+
+# ---- the mixers: a lost signal ends every kernel with a recorded timeout ----
+
+@pytest.fixture(scope="module")
+def dmesa():
+    """The binding on the debug library."""
+    import importlib.util
+    from test_sequence_layer_b200 import build as b, mesa
+    spec = importlib.util.spec_from_file_location("mesa_on_debug_library", mesa.__file__)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m._LIB_PATH = b.build(debug=True)
+    return m
+
+
+def after_a_lost_signal(m, launches, call):
+    """`call` with and without the fault: the timeout is seen, and the next call gives what the first gave."""
+    want = call()
+    assert m.get_error() == MESA_OK
+    assert m._load().mesa_debug_lose_signal(launches) == MESA_OK
+    call()
+    assert m.get_error() == MESA_ERR_DEVICE_TIMEOUT
+    assert m.get_error() == MESA_OK
+    for a, b in zip(want, call()):
+        assert torch.equal(a, b)
+    assert m.get_error() == MESA_OK
+
+
+# one CTA, a cluster of two whose CTAs wait for one another, sixteen over many tiles
+@pytest.mark.parametrize("B,T,D", [(1, 100, 64), (1, 300, 64), (1, 5000, 64)])
+def test_recurrence_gives_up(dmesa, B, T, D):
+    g = torch.Generator().manual_seed(1)
+    x, ga, gx, dy = (torch.randn(B, T, D, generator=g).cuda().bfloat16() for _ in range(4))
+    lam = (torch.randn(D, generator=g) - 4).cuda()
+    after_a_lost_signal(dmesa, 1, lambda: dmesa.lru_forward(x, ga, gx, lam, return_state=True, return_saved=True))
+    saved = dmesa.lru_forward(x, ga, gx, lam, return_saved=True)[1]
+    after_a_lost_signal(dmesa, 1, lambda: dmesa.lru_backward(x, ga, gx, lam, dy, saved=saved))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_gives_up(dmesa, d):
+    g = torch.Generator().manual_seed(2)
+    q, k, v, do = (torch.randn(1, 2, 900, d, generator=g).cuda().bfloat16() for _ in range(4))
+    kw = dict(window=300, sinks=4)
+    after_a_lost_signal(dmesa, 1, lambda: dmesa.swa_forward(q, k, v, return_lse=True, **kw))
+    out, lse = dmesa.swa_forward(q, k, v, return_lse=True, **kw)
+    for launches in (1, 2):                              # dk and dv; then dq as well
+        after_a_lost_signal(dmesa, launches, lambda: dmesa.swa_backward(q, k, v, out, lse, do, **kw))
