@@ -439,23 +439,26 @@ cudaError_t bwd(const SwaBackwardArgs& a, const float* delta, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t fwd_d(const SwaArgs& a, cudaStream_t st) {
+// bf16 of 64 and 128 columns never comes here: the tensor cores take it
+cudaError_t fwd_any(const SwaArgs& a, cudaStream_t st) {
+    using bf = __nv_bfloat16;
+    if (a.dtype == MESA_BF16) return a.d == 16 ? fwd<bf, 16>(a, st) : fwd<bf, 32>(a, st);
     switch (a.d) {
-        case 16: return fwd<T, 16>(a, st);
-        case 32: return fwd<T, 32>(a, st);
-        case 64: return fwd<T, 64>(a, st);
-        default: return fwd<T, 128>(a, st);
+        case 16: return fwd<float, 16>(a, st);
+        case 32: return fwd<float, 32>(a, st);
+        case 64: return fwd<float, 64>(a, st);
+        default: return fwd<float, 128>(a, st);
     }
 }
 
-template <typename T>
-cudaError_t bwd_d(const SwaBackwardArgs& a, const float* delta, cudaStream_t st) {
+cudaError_t bwd_any(const SwaBackwardArgs& a, const float* delta, cudaStream_t st) {
+    using bf = __nv_bfloat16;
+    if (a.f.dtype == MESA_BF16) return a.f.d == 16 ? bwd<bf, 16>(a, delta, st) : bwd<bf, 32>(a, delta, st);
     switch (a.f.d) {
-        case 16: return bwd<T, 16>(a, delta, st);
-        case 32: return bwd<T, 32>(a, delta, st);
-        case 64: return bwd<T, 64>(a, delta, st);
-        default: return bwd<T, 128>(a, delta, st);
+        case 16: return bwd<float, 16>(a, delta, st);
+        case 32: return bwd<float, 32>(a, delta, st);
+        case 64: return bwd<float, 64>(a, delta, st);
+        default: return bwd<float, 128>(a, delta, st);
     }
 }
 
@@ -480,7 +483,7 @@ cudaError_t swa_delta(const SwaArgs& a, const void* dout, float* delta, cudaStre
 
 cudaError_t swa_forward_simt(const SwaArgs& a, cudaStream_t st) {
     LaunchTimer lt(kKindSwa, st);
-    return a.dtype == MESA_F32 ? fwd_d<float>(a, st) : fwd_d<__nv_bfloat16>(a, st);
+    return fwd_any(a, st);
 }
 
 cudaError_t swa_backward_simt(const SwaBackwardArgs& a, cudaStream_t st) {
@@ -488,7 +491,7 @@ cudaError_t swa_backward_simt(const SwaBackwardArgs& a, cudaStream_t st) {
     float* delta = static_cast<float*>(a.workspace);
     cudaError_t e = swa_delta(a.f, a.dout, delta, st);
     if (e != cudaSuccess) return e;
-    return a.f.dtype == MESA_F32 ? bwd_d<float>(a, delta, st) : bwd_d<__nv_bfloat16>(a, delta, st);
+    return bwd_any(a, delta, st);
 }
 
 }  // namespace mesa

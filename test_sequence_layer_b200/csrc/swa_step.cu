@@ -631,12 +631,13 @@ cudaError_t launch_cluster(F* kernel, const SwaStepArgs& a, int hgroups, int slo
     return cudaLaunchKernelEx(&cfg, kernel, a, splits);
 }
 
+bool use_mma(const SwaStepArgs& a) { return a.dtype == MESA_BF16 && (a.d == 64 || a.d == 128); }
+
 // Both launches against the cluster's one, events around a call: 15.4 us against
 // 13.2 at 4 MB (8 heads of 1028 slots), 15.4 against 12.4 at 7.9 MB (32 heads of
 // 504), 15.3 against 16.1 at 8.0 MB (8 heads of 2048), 20 against 30 at 16.8 MB.
 bool use_stream(const SwaStepArgs& a) {
-    if (a.dtype != MESA_BF16 || (a.d != 64 && a.d != 128)) return false;
-    return (long long)a.B * a.Hkv * ((long long)a.sinks + a.window) * a.d * 4 >= (8LL << 20);
+    return use_mma(a) && (long long)a.B * a.Hkv * ((long long)a.sinks + a.window) * a.d * 4 >= (8LL << 20);
 }
 
 template <int ROWS, int D>
@@ -673,13 +674,15 @@ cudaError_t step_simt_d(const SwaStepArgs& a, cudaStream_t st) {
                           kSimtThreads, 0, st);
 }
 
-template <typename T>
+// bf16 of 64 and 128 columns never comes here: the matrix instructions take it
 cudaError_t step_simt(const SwaStepArgs& a, cudaStream_t st) {
+    using bf = __nv_bfloat16;
+    if (a.dtype == MESA_BF16) return a.d == 16 ? step_simt_d<bf, 16>(a, st) : step_simt_d<bf, 32>(a, st);
     switch (a.d) {
-        case 16: return step_simt_d<T, 16>(a, st);
-        case 32: return step_simt_d<T, 32>(a, st);
-        case 64: return step_simt_d<T, 64>(a, st);
-        default: return step_simt_d<T, 128>(a, st);
+        case 16: return step_simt_d<float, 16>(a, st);
+        case 32: return step_simt_d<float, 32>(a, st);
+        case 64: return step_simt_d<float, 64>(a, st);
+        default: return step_simt_d<float, 128>(a, st);
     }
 }
 
@@ -693,11 +696,10 @@ size_t swa_step_workspace_bytes(const SwaStepArgs& a) {
 
 cudaError_t swa_step(const SwaStepArgs& a, cudaStream_t st) {
     LaunchTimer lt(kKindSwaStep, st);
-    if (a.dtype == MESA_F32) return step_simt<float>(a, st);
+    if (!use_mma(a)) return step_simt(a, st);
     const bool wide = a.Hq / a.Hkv > 8;
     if (a.d == 128) return wide ? step_mma<16, 128>(a, st) : step_mma<8, 128>(a, st);
-    if (a.d == 64) return wide ? step_mma<16, 64>(a, st) : step_mma<8, 64>(a, st);
-    return step_simt<__nv_bfloat16>(a, st);
+    return wide ? step_mma<16, 64>(a, st) : step_mma<8, 64>(a, st);
 }
 
 cudaError_t swa_cache_fill(const void* k, const void* v, void* kc, void* vc, const int32_t* lens, int B, int Hkv,

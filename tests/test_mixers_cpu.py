@@ -173,3 +173,18 @@ def test_reference_attention_agrees_with_autograd_and_loops():
     assert torch.allclose(r["out"][0], out, rtol=1e-10, atol=1e-12)
     for n, w in zip(("dq", "dk", "dv"), want):
         assert torch.allclose(r[n][0], w, rtol=1e-10, atol=1e-12), n
+
+
+def test_no_kernel_that_no_call_reaches(lib):
+    """bf16 of 64 and 128 columns runs on matrix instructions alone: the library holds no fp32-arithmetic kernel for it."""
+    import shutil
+    import subprocess
+    from test_sequence_layer_b200 import mesa
+    if not shutil.which("nm"):
+        pytest.skip("needs nm")
+    names = subprocess.run(["nm", "-C", mesa.library_path()], check=True, capture_output=True, text=True).stdout
+    for kernel in ("swa_fwd_kernel", "swa_dq_kernel", "swa_dkv_kernel", "swa_dkv_sum_kernel", "swa_step_simt_kernel"):
+        for d in (16, 32):
+            assert f"{kernel}<__nv_bfloat16, {d}>" in names, (kernel, d)
+        for d in (64, 128):
+            assert f"{kernel}<float, {d}>" in names and f"{kernel}<__nv_bfloat16, {d}>" not in names, (kernel, d)
