@@ -433,3 +433,127 @@ def test_cache_of_the_most_slots(mesa):
     assert mesa.get_error() == 0
     del kc, vc
     torch.cuda.empty_cache()
+
+
+# ---- decode over caches of 8 MB and more: equal shares of all runs of 64 slots, parts joined by a second launch ----
+
+SHARES = [  # (B, Hq, Hkv, window, sinks); all of 8 MB and more at d = 64
+    (48, 8, 4, 600, 4),          # several parts a head, joined by small blocks
+    (40, 9, 1, 1000, 0),         # a group above eight
+    (4, 24, 1, 9000, 5),         # two blocks of heads in a group, many parts a head, joined by large blocks
+    (1, 2, 1, 40000, 4),         # one head over all SMs
+    (300, 4, 2, 64, 0),          # one run a head, two heads a share: no parts at all
+    (30, 10, 10, 130, 128),      # many heads of few runs
+    (90, 16, 1, 272, 128),       # sinks over two runs
+]
+
+
+def share_positions(trial, B, cap, g):
+    """Positions of a batch: full and young rows mixed, edges of a run, idle rows, one row alone, none."""
+    edges = [0, cap - 1, 63, -1, 64, 4 * cap + 7, 127, 1, -5, 2 ** 31 - 1, cap, cap // 2]
+    if trial == 0:
+        return [edges[b % len(edges)] for b in range(B)]
+    if trial == 1:                                       # a short one between long ones, idle first and last
+        pos = [2 * cap + 3 if b % 3 else b % 5 for b in range(B)]
+        if B > 2:
+            pos[0] = pos[-1] = -1
+        return pos
+    if trial == 2:
+        return torch.randint(0, 2 * cap, (B,), generator=g).tolist()
+    if trial == 3:                                       # the last row alone
+        return [-1] * (B - 1) + [cap + 1]
+    return [-1 - b for b in range(B)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("case", SHARES, ids=lambda c: "-".join(map(str, c)))
+def test_step_in_equal_shares(mesa, case, d):
+    B, Hq, Hkv, window, sinks = case
+    cap = window + sinks
+    assert B * Hkv * cap * d * 4 >= 8 << 20
+    kw = dict(window=window, sinks=sinks)
+    g = torch.Generator().manual_seed(cap + d)
+    kc, vc = (torch.randn(B, Hkv, cap, d, generator=g).cuda().bfloat16() for _ in range(2))
+    assert mesa._load().mesa_swa_step_workspace_size(B, Hq, Hkv, d, window, sinks, 1) > 0
+    for trial in range(5):
+        pos = share_positions(trial, B, cap, g)
+        q = torch.randn(B, Hq, d, generator=g).cuda().bfloat16()
+        k, v = (torch.randn(B, Hkv, d, generator=g).cuda().bfloat16() for _ in range(2))
+        wk, wv, ik, iv = kc.clone(), vc.clone(), kc.clone(), vc.clone()
+        for b, p in enumerate(pos):                      # NaN where nothing may be read
+            if p >= 0:
+                slot = p if p < sinks else sinks + (p - sinks) % window
+                wk[b, :, slot], wv[b, :, slot] = k[b], v[b]
+                for t in (ik, iv):
+                    t[b, :, p + 1:] = float("nan")
+                    t[b, :, slot] = float("nan")
+            else:
+                ik[b], iv[b] = float("nan"), float("nan")
+        gk, gv = ik.clone(), iv.clone()
+        pd = torch.tensor(pos, dtype=torch.int32, device="cuda")
+        out = torch.full_like(q, float("nan"))
+        mesa.swa_step(q, k, v, gk, gv, pd, out=out, **kw)
+        for b, p in enumerate(pos):
+            one = slice(b, b + 1)
+            if p < 0:
+                assert torch.count_nonzero(out[b]) == 0 and torch.isnan(gk[b]).all() and torch.isnan(gv[b]).all()
+                continue
+            n = min(p + 1, cap)
+            assert torch.equal(gk[b, :, :n], wk[b, :, :n]) and torch.equal(gv[b, :, :n], wv[b, :, :n])
+            assert torch.isnan(gk[b, :, n:]).all() and torch.isnan(gv[b, :, n:]).all()
+            want, bound = step_ref(q[one], wk[one], wv[one], pd[one], window, sinks, True)
+            ref.check(out[one], want, bound, f"trial {trial} row {b}")
+        assert torch.equal(out, mesa.swa_step(q, k, v, ik, iv, pd, **kw))          # no order in it
+        kc, vc = wk, wv
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,d,window", [(24, 8, 4, 128, 300), (2, 12, 1, 64, 20000)])
+def test_captured_shares_follow_pos(mesa, B, Hq, Hkv, d, window):
+    """Both launches of a step in a graph, replayed while the positions advance."""
+    sinks, T = 3, 60
+    cap = window + sinks
+    assert B * Hkv * cap * d * 4 >= 8 << 20
+    g = torch.Generator().manual_seed(51)
+    q = torch.randn(T, B, Hq, d, generator=g).cuda().bfloat16()
+    k, v = (torch.randn(T, B, Hkv, d, generator=g).cuda().bfloat16() for _ in range(2))
+    first = torch.randint(0, 2 * cap, (B,), generator=g).int().cuda()
+    first[0] = -3                                        # idle for three steps, then a first token
+    caches = [torch.randn(B, Hkv, cap, d, generator=g).cuda().bfloat16() for _ in range(2)]
+    want, eager, pos = [], [c.clone() for c in caches], first.clone()
+    for t in range(T):
+        want.append(mesa.swa_step(q[t], k[t], v[t], *eager, pos, window=window, sinks=sinks))
+        pos += 1
+    qi, ki, vi, pos = q[0].clone(), k[0].clone(), v[0].clone(), first.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = mesa.swa_step(qi, ki, vi, *caches, pos, window=window, sinks=sinks)
+        pos.add_(1)
+    for t in range(T):
+        for dst, src in ((qi, q), (ki, k), (vi, v)):
+            dst.copy_(src[t])
+        graph.replay()
+        assert torch.equal(out, want[t]), t
+    for a, b in zip(caches, eager):
+        assert torch.equal(a, b)
+
+
+def test_shares_on_two_streams(mesa):
+    """Steps that overlap, each with its own caches and workspace."""
+    B, Hq, Hkv, d, window, sinks = 20, 8, 2, 128, 1000, 4
+    g = torch.Generator().manual_seed(52)
+    sets = []
+    for _ in range(2):
+        q = torch.randn(B, Hq, d, generator=g).cuda().bfloat16()
+        k, v = (torch.randn(B, Hkv, d, generator=g).cuda().bfloat16() for _ in range(2))
+        kc, vc = (torch.randn(B, Hkv, window + sinks, d, generator=g).cuda().bfloat16() for _ in range(2))
+        sets.append((q, k, v, kc, vc, torch.randint(0, 3000, (B,), generator=g).int().cuda()))
+    want = [mesa.swa_step(*s, window=window, sinks=sinks) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(10):
+        for i, (st, s) in enumerate(zip(streams, sets)):
+            got[i].append(mesa.swa_step(*s, window=window, sinks=sinks, stream=st))
+    torch.cuda.synchronize()
+    for w, outs in zip(want, got):
+        assert all(torch.equal(w, o) for o in outs)
