@@ -284,3 +284,54 @@ def test_state_in_place(mesa, B, T, D):
         assert lib.mesa_lru_forward(x.data_ptr(), ga.data_ptr(), gx.data_ptr(), lam.data_ptr(), B, T, D, 1, h.data_ptr(),
                                     y.data_ptr(), h.data_ptr(), None, stream) == 0
         assert torch.equal(h, wT) and torch.equal(y, want)
+
+
+# Walks of five tiles and more a CTA: clusters of 16, 8, 4, 2 and none, by tensor copies and by 4-byte copies
+LONG = [("bf16", 1, 10277, 64), ("bf16", 3, 4173, 512), ("bf16", 3, 2200, 1024), ("bf16", 5, 1100, 1024),
+        ("bf16", 10, 1100, 1024), ("bf16", 1, 10277, 66), ("f32", 1, 10277, 32), ("f32", 2, 4173, 512),
+        ("f32", 5, 1100, 520), ("f32", 1, 10277, 33), ("f32", 5, 1100, 1003)]
+
+
+@pytest.mark.parametrize("dtype,B,T,D", LONG)
+def test_long_walks(mesa, dtype, B, T, D):
+    x, ga, gx, lam, dy, h0, dh = inputs(B, T, D, dtype, seed=T + D)
+    y, hT, saved = mesa.lru_forward(x, ga, gx, lam, h0=h0, return_state=True, return_saved=True)
+    want, wT, ey, eT = ref.lru(x, ga, gx, lam, h0)
+    ref.check(y, want, ey, "y")
+    ref.check(hT, wT, eT, "h_T")
+    at, eat = want[:, 63:-1:64], ey[:, 63:-1:64]
+    ref.check(saved[:, 1:], at, eat, "saved")
+    del want, ey
+    got = mesa.lru_backward(x, ga, gx, lam, dy, saved=saved, dh_T=dh)
+    want, bound = ref.lru_grads(x, ga, gx, lam, h0, dy, dh)
+    for n, o, w, b in zip(("dx", "dgate_a", "dgate_x", "dlam", "dh0"), got, want, bound):
+        ref.check(o, w, b, n)
+    for o, o2 in zip(got, mesa.lru_backward(x, ga, gx, lam, dy, saved=saved, dh_T=dh)):
+        assert torch.equal(o, o2)
+    assert mesa.get_error() == 0
+
+
+@pytest.mark.parametrize("lams", [(-120.0, -95.0, -60.0, -25.0, -15.0, -3.0, 0.0, 5.0, 60.0),
+                                  (-120.0, -95.0, -60.0, -25.0, -15.0, -8.0, -6.0, -5.0, -4.0)],
+                         ids=["any decay", "slow decays"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_at_extreme_gates(mesa, dtype, lams):
+    """The gradients' values where gates are closed, open and saturated."""
+    B, T = 1, 200
+    vals = torch.tensor([-float("inf"), -90.0, -60.0, -30.0, -10.0, 0.0, 10.0, 40.0, 100.0, float("inf")])
+    lams = torch.tensor(lams)
+    D = len(vals) * len(lams)
+    x, ga, gx, lam, dy, h0, dh = inputs(B, T, D, dtype, seed=3)
+    ga[:] = vals.repeat(len(lams)).to(ga)
+    gx[:] = vals.flip(0).repeat(len(lams)).to(gx)
+    gx[:, ::2] = torch.randn(100, D, generator=torch.Generator().manual_seed(5)).to(gx)
+    lam[:] = lams.repeat_interleave(len(vals)).to(lam)
+    _, saved = mesa.lru_forward(x, ga, gx, lam, h0=h0, return_saved=True)
+    got = mesa.lru_backward(x, ga, gx, lam, dy, saved=saved, dh_T=dh)
+    want, bound = ref.lru_grads(x, ga.float().clamp(-104, 104), gx.float().clamp(-104, 104), lam, h0, dy, dh)
+    # A sigmoid below 2^-126 counts as 0, and 1 - a^2 is held to 1e-36: m = sqrt(2 * 8 softplus(60) * 2^-126) < 4e-18
+    # may be lost, and an i below 2^-63. Times x, h (below 8 and 100) and g, sums of up to T + 1 terms below 6 (1206):
+    # 4e-18 * 100 * 1206 < 5e-13 of an element, T of them in dlam.
+    eps = 5e-13
+    for n, o, w, b in zip(("dx", "dgate_a", "dgate_x", "dlam", "dh0"), got, want, bound):
+        ref.check(o, w, b + (T * eps if n == "dlam" else eps), n)
