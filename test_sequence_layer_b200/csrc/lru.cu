@@ -808,9 +808,14 @@ int cluster_size(long long blocks, int tiles) {
     return n;
 }
 
-template <typename F, typename... A>
-cudaError_t launch_cluster(F* kernel, unsigned grid, int threads, int ncta, int smem, cudaStream_t st, A... args) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// Shared memory of a launch: the stager's, and the maps of ncta CTAs. The
+// kernel's limit is set to what any launch may ask for, always: another host
+// thread may be about to launch it for a larger cluster.
+template <int VEC, typename F, typename... A>
+cudaError_t launch_cluster(F* kernel, unsigned grid, int threads, int ncta, int stager_bytes, cudaStream_t st, A... args) {
+    const int smem = stager_bytes + peer_bytes<VEC>(ncta);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         stager_bytes + peer_bytes<VEC>(kLruMaxCluster));
     if (e == cudaSuccess && ncta > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -852,9 +857,8 @@ cudaError_t forward(const LruArgs& a, const Plan& pl, unsigned* err, cudaStream_
     if (LOAD == kTensor && (!channel_map(&m[0], a, a.x, S::kTokens) || !channel_map(&m[1], a, a.ga, S::kTokens) ||
                             !channel_map(&m[2], a, a.gx, S::kTokens)))
         return cudaErrorInvalidValue;
-    return launch_cluster(lru_forward_kernel<T, VEC, LOAD, S>, pl.grid, S::NW * 32, pl.ncta,
-                          Stager<T, VEC, 3, LOAD, S>::kBytes + peer_bytes<VEC>(pl.ncta), st, m[0], m[1], m[2], a, pl.groups,
-                          pl.ncta, err);
+    return launch_cluster<VEC>(lru_forward_kernel<T, VEC, LOAD, S>, pl.grid, S::NW * 32, pl.ncta,
+                               Stager<T, VEC, 3, LOAD, S>::kBytes, st, m[0], m[1], m[2], a, pl.groups, pl.ncta, err);
 }
 
 template <typename T, int VEC, int LOAD>
@@ -872,9 +876,9 @@ cudaError_t backward(const LruBackwardArgs& q, unsigned* err, cudaStream_t st) {
                             !channel_map(&m[2], a, a.gx, S::kTokens) || !channel_map(&m[3], a, q.dy, S::kTokens)))
         return cudaErrorInvalidValue;
     const Plan pl = plan(a.B, a.T, a.D, VEC, S::kTokens);
-    cudaError_t e = launch_cluster(lru_backward_kernel<T, VEC, LOAD, S>, pl.grid, S::NW * 32, pl.ncta,
-                                   Stager<T, VEC, 4, LOAD, S>::kBytes + peer_bytes<VEC>(pl.ncta), st, m[0], m[1], m[2],
-                                   m[3], q, pl.groups, pl.ncta, err);
+    cudaError_t e = launch_cluster<VEC>(lru_backward_kernel<T, VEC, LOAD, S>, pl.grid, S::NW * 32, pl.ncta,
+                                        Stager<T, VEC, 4, LOAD, S>::kBytes, st, m[0], m[1], m[2], m[3], q, pl.groups,
+                                        pl.ncta, err);
     if (e != cudaSuccess) return e;
     lru_dlambda_kernel<<<(a.D + 31) / 32, dim3(32, 8), 0, st>>>(q.partial, (size_t)a.B * pl.ncta, a.D, a.lambda,
                                                                q.dlambda);

@@ -335,3 +335,36 @@ def test_gradients_at_extreme_gates(mesa, dtype, lams):
     eps = 5e-13
     for n, o, w, b in zip(("dx", "dgate_a", "dgate_x", "dlam", "dh0"), got, want, bound):
         ref.check(o, w, b + (T * eps if n == "dlam" else eps), n)
+
+
+def test_two_host_threads(mesa):
+    """Calls from two host threads whose clusters, and so whose shared memory, differ in size."""
+    import threading
+    sets = [inputs(1, T, 64, "bf16", seed=T) for T in (300, 3000)]        # clusters of 2 (forward) or 4, and of 16
+
+    def once(s):
+        x, ga, gx, lam, dy, h0, dh = s
+        y, saved = mesa.lru_forward(x, ga, gx, lam, h0=h0, return_saved=True)
+        return (y,) + mesa.lru_backward(x, ga, gx, lam, dy, saved=saved, dh_T=dh)
+    want = [once(s) for s in sets]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def loop(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                torch.cuda.current_stream().wait_stream(torch.cuda.default_stream())
+                for _ in range(2000):
+                    got = once(sets[i])
+                torch.cuda.current_stream().synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                wrong.append((i, "values"))
+        except Exception as e:                                            # a refused launch
+            wrong.append((i, str(e)))
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+    assert mesa.get_error() == 0
