@@ -394,7 +394,12 @@ swa_tc_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
             if (q.live) l = exchange(l2.x + l2.y, [](float u, float v) { return u + v; });
             // A tile past the last query waits as well: without it its warps would
             // arrive on o_free items ahead and complete phases in the others' place.
-            if (ok) ok = swa::wait_bar(o_full, k & 1);
+            // It waits for the whole item, about 2 us a key tile, so it is given a
+            // second for every 2^17 of them.
+            if (ok) {
+                int more = q.live ? 0 : kt.n >> 17;
+                while (!(ok = swa::wait_bar(o_full, k & 1)) && more > 0) --more;
+            }
             if (q.live) {
                 const float inv = 1.f / l;
                 tc_fence_after();

@@ -557,3 +557,54 @@ def test_shares_on_two_streams(mesa):
     torch.cuda.synchronize()
     for w, outs in zip(want, got):
         assert all(torch.equal(w, o) for o in outs)
+
+
+@pytest.mark.parametrize("d", [64])
+def test_one_query_over_two_hundred_million_keys(mesa, d):
+    """A pair of tiles whose second is empty, over more key tiles than one bounded wait lasts."""
+    S = 200_000_000
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 2 * S * d * 2 + (2 << 30):
+        pytest.skip("needs 54 GB of device memory")
+    k, v = (torch.zeros(1, 1, S, d, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    at = torch.tensor([0, 5, 127, 128, 31_234_567, 50_000_000, S - 129, S - 1], device="cuda")
+    g = torch.Generator().manual_seed(61)
+    k[0, 0, at] = 4.0                                    # scores of 32, all others 0
+    v[0, 0, at] = torch.randn(len(at), d, generator=g).cuda().bfloat16()
+    q = torch.ones(1, 1, 1, d, device="cuda", dtype=torch.bfloat16)
+    out, lse = mesa.swa_forward(q, k, v, window=S, return_lse=True)
+    assert mesa.get_error() == 0
+    vd = v[0, 0, at].double()
+    rest = (S - len(at)) * 2.718281828459045 ** -32      # weights of e^-32, 2.6e-6 together, lost or not
+    want = vd.sum(0) / (len(at) + rest)
+    # P rounds to bf16 (1 = e^0 exactly, on a reference that a row with larger weights moves to its maximum); fp32 sums
+    ref.check(out[0, 0, 0], want, 2.0 ** -17 * vd.abs().sum(0), "out")
+    assert abs(float(lse[0, 0, 0]) - 32 - torch.log(torch.tensor(len(at) + rest, dtype=torch.float64)).item()) < 40 * 2.0 ** -22
+    del k, v
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sequences_past_32_bit_offsets(mesa, dtype):
+    """The last rows of the last head of tensors of more than 2^31 elements, and a key head summed over all query heads."""
+    Hq, T, d, window, rows = 66, 256 * 1024 + 5, 128, 16, 200
+    assert Hq * T * d > 2 ** 31
+    torch.cuda.empty_cache()
+    g = torch.Generator(device="cuda").manual_seed(62)
+    q, do = (torch.empty(1, Hq, T, d, device="cuda", dtype=DT[dtype]).normal_(generator=g) for _ in range(2))
+    k, v = (torch.empty(1, Hq, T, d, device="cuda", dtype=DT[dtype]).normal_(generator=g) for _ in range(2))
+    out, lse = mesa.swa_forward(q, k, v, window=window, return_lse=True)
+    dq, dk, dv = mesa.swa_backward(q, k, v, out, lse, do, window=window)
+    assert mesa.get_error() == 0
+    head, last = slice(Hq - 1, Hq), slice(T - rows, T)
+    seen = slice(T - rows - window + 1, T)               # the keys that these rows see
+    want = ref.swa(q[:, head, last], k[:, head, seen], v[:, head, seen], window, 0, matrix=dtype == "bf16",
+                   dout=do[:, head, last])
+    ref.check(out[:, head, last], *want["out"], "out")
+    ref.check(lse[:, head, last], *want["lse"], "lse")
+    ref.check(dq[:, head, last], *want["dq"], "dq")
+    for n, t in (("dk", dk), ("dv", dv)):                # keys whose queries are all among the rows
+        w, b = want[n]
+        ref.check(t[:, head, last], w[:, :, window - 1:], b[:, :, window - 1:], n)
+    del q, k, v, do, out, dq, dk, dv
+    torch.cuda.empty_cache()
