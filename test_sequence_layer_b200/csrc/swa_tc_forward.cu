@@ -54,8 +54,17 @@ bool encode_map(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, const 
     const cuuint64_t dims[3] = {(cuuint64_t)x, (cuuint64_t)y, (cuuint64_t)z};
     const cuuint64_t strides[2] = {(cuuint64_t)x * elem_bytes, (cuuint64_t)x * elem_bytes * y};
     const cuuint32_t box[3] = {(cuuint32_t)bx, (cuuint32_t)by, 1}, one[3] = {1, 1, 1};
-    return encode(m, type, 3, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    auto attempt = [&] {
+        return encode(m, type, 3, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = attempt();
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {           // a host thread's first call: its device has no context here yet
+        int dev;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
+        r = attempt();
+    }
+    return r == CUDA_SUCCESS;
 }
 
 bool make_map(CUtensorMap* m, const void* base, int d, int rows, int heads, int box_rows) {

@@ -608,3 +608,46 @@ def test_sequences_past_32_bit_offsets(mesa, dtype):
         ref.check(t[:, head, last], w[:, :, window - 1:], b[:, :, window - 1:], n)
     del q, k, v, do, out, dq, dk, dv
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("call", ["forward", "backward", "step", "lru_forward", "lru_backward"])
+def test_first_call_of_a_host_thread(mesa, call):
+    """A thread that has made no CUDA call before, once the library has been used by another."""
+    import threading
+    lib = mesa._load()
+    q, k, v, do = inputs(1, 2, 1, 200, 200, 64, "bf16", seed=71)
+    out, lse = mesa.swa_forward(q, k, v, window=50, return_lse=True)
+    grads = mesa.swa_backward(q, k, v, out, lse, do, window=50)
+    x, ga, gx, dy = (t.view(1, 400, 64) for t in (q, do, out, out))
+    lam = torch.full((64,), -4.0, device="cuda")
+    y, saved = mesa.lru_forward(x, ga, gx, lam, return_saved=True)
+    lgrads = mesa.lru_backward(x, ga, gx, lam, dy, saved=saved)
+    kc, vc = (torch.zeros(1, 1, 200, 64, device="cuda", dtype=q.dtype) for _ in range(2))
+    pos = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o1 = mesa.swa_step(q[:, :, 0].contiguous(), k[:, :, 0].contiguous(), v[:, :, 0].contiguous(), kc, vc, pos, window=200)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    p = [t.data_ptr() for t in (q, k, v, out, lse, do)]
+    new = {"forward": (out, lse), "backward": grads, "step": (o1,), "lru_forward": (y,), "lru_backward": lgrads}[call]
+    got = [torch.full_like(t, float("nan")) for t in new]
+    g = [t.data_ptr() for t in got]
+    first = [t[:, :, 0].contiguous() for t in (q, k, v)]
+    lp = [t.data_ptr() for t in (x, ga, gx, lam)] + [1, 400, 64, 1, None]
+    torch.cuda.synchronize()
+    scale = 64 ** -0.5
+    run = {
+        "forward": lambda: lib.mesa_swa_forward(*p[:3], 1, 2, 1, 200, 200, 64, 50, 0, scale, 1, *g, None),
+        "backward": lambda: lib.mesa_swa_backward(*p, 1, 2, 1, 200, 200, 64, 50, 0, scale, 1, *g, ws.data_ptr(), ws.numel(), None),
+        "step": lambda: lib.mesa_swa_step(*[t.data_ptr() for t in first], kc.data_ptr(), vc.data_ptr(), pos.data_ptr(), 1, 2, 1,
+                                          64, 200, 0, scale, 1, *g, ws.data_ptr(), ws.numel(), None),
+        "lru_forward": lambda: lib.mesa_lru_forward(*lp, *g, None, None, None),
+        "lru_backward": lambda: lib.mesa_lru_backward(*lp, saved.data_ptr(), dy.data_ptr(), None, *g, ws.data_ptr(), ws.numel(),
+                                                      None),
+    }[call]
+    status = []
+    t = threading.Thread(target=lambda: status.append(run()))
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert status == [0]
+    for a, b in zip(got, new):
+        assert torch.equal(a, b)
