@@ -368,3 +368,29 @@ def test_two_host_threads(mesa):
         t.join()
     assert not wrong, wrong
     assert mesa.get_error() == 0
+
+
+def test_two_host_threads_launch(mesa):
+    """The same at the rate of the C ABI: no launch of a larger cluster is refused because a smaller one was prepared meanwhile."""
+    import threading
+    lib, refused, keep, args = mesa._load(), [0, 0], [], []
+    for T in (300, 3000):
+        x, ga, gx, lam, _, _, _ = inputs(1, T, 64, "bf16", seed=T)
+        y, stream = torch.empty_like(x), torch.cuda.Stream()
+        keep.append((x, ga, gx, lam, y, stream))
+        args.append((x.data_ptr(), ga.data_ptr(), gx.data_ptr(), lam.data_ptr(), 1, T, 64, 1, None, y.data_ptr(), None, None,
+                     stream.cuda_stream))
+    torch.cuda.synchronize()
+
+    def loop(i):
+        for _ in range(60000):
+            refused[i] += lib.mesa_lru_forward(*args[i]) != 0
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert refused == [0, 0]
+    for x, ga, gx, lam, y, _ in keep:
+        assert torch.equal(y, mesa.lru_forward(x, ga, gx, lam))
