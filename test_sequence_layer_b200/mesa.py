@@ -469,11 +469,13 @@ def _first(name, t, dims):
 
 class _On:
     """Runs a call on the tensors' device; what it allocates belongs to its
-    stream. `raw` is that stream's handle."""
+    stream. `raw` is that stream's handle. Where the caller names a stream the
+    tensors are marked as used on it: memory that the caller drops while the
+    call is still to run is not handed out again before it has."""
 
     __slots__ = ("contexts", "raw")
 
-    def __init__(self, index, stream):
+    def __init__(self, index, stream, *tensors):
         self.contexts = ()
         if torch.cuda.current_device() != index:
             self.contexts = (torch.cuda.device(index),)
@@ -484,6 +486,9 @@ class _On:
                 raise ValueError(f"stream belongs to cuda:{stream.device_index}, the tensors to cuda:{index}")
             self.contexts += (torch.cuda.stream(stream),)
             self.raw = stream.cuda_stream
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
 
     def __enter__(self):
         for c in self.contexts:
@@ -535,7 +540,7 @@ def lru_forward(x, gate_a, gate_x, lam, *, h0=None, y=None, return_state=False, 
         _arg("h0", h0, (B, D), torch.float32, index)
     if y is not None:
         _arg("y", y, x.shape, x.dtype, index)
-    with _On(index, stream) as raw:
+    with _On(index, stream, x, gate_a, gate_x, lam, h0, y) as raw:
         y = torch.empty_like(x) if y is None else y
         h_T = torch.empty((B, D), dtype=torch.float32, device=dev) if return_state else None
         saved = torch.empty((B, -(-T // 64), D), dtype=torch.float32, device=dev) if return_saved else None
@@ -561,7 +566,7 @@ def lru_backward(x, gate_a, gate_x, lam, dy, *, h0=None, saved=None, dh_T=None, 
         _arg("saved", saved, (B, -(-T // 64), D), torch.float32, index)
     if dh_T is not None:
         _arg("dh_T", dh_T, (B, D), torch.float32, index)
-    with _On(index, stream) as raw:
+    with _On(index, stream, x, gate_a, gate_x, lam, dy, h0, saved, dh_T, workspace) as raw:
         dx, dga, dgx = (torch.empty_like(x) for _ in range(3))
         dlam = torch.empty(D, dtype=torch.float32, device=dev)
         dh0 = torch.empty((B, D), dtype=torch.float32, device=dev)
@@ -586,7 +591,7 @@ def lru_step(x, gate_a, gate_x, lam, h, *, h_out=None, y=None, stream=None):
         _arg("h_out", h_out, (B, D), torch.float32, index)
     if y is not None:
         _arg("y", y, x.shape, x.dtype, index)
-    with _On(index, stream) as raw:
+    with _On(index, stream, x, gate_a, gate_x, lam, h, h_out, y) as raw:
         y = torch.empty_like(x) if y is None else y
         _check(lib.mesa_lru_step(_p(x), _p(gate_a), _p(gate_x), _p(lam), B, D, _dtype_code(x), _p(h),
                                  _p(h if h_out is None else h_out), _p(y), raw), "mesa_lru_step")
@@ -631,7 +636,7 @@ def swa_forward(q, k, v, *, window, sinks=0, scale=None, out=None, return_lse=Fa
     (B, Hq, T, d), (_, Hkv, S, _), dev = q.shape, k.shape, q.device
     if out is not None:
         _arg("out", out, q.shape, q.dtype, index)
-    with _On(index, stream) as raw:
+    with _On(index, stream, q, k, v, out) as raw:
         out = torch.empty_like(q) if out is None else out
         lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev) if return_lse else None
         _check(lib.mesa_swa_forward(_p(q), _p(k), _p(v), B, Hq, Hkv, T, S, d, _size("window", window), _size("sinks", sinks),
@@ -649,7 +654,7 @@ def swa_backward(q, k, v, out, lse, dout, *, window, sinks=0, scale=None, worksp
     _arg("out", out, q.shape, q.dtype, index)
     _arg("lse", lse, (B, Hq, T), torch.float32, index)
     _arg("dout", dout, q.shape, q.dtype, index)
-    with _On(index, stream) as raw:
+    with _On(index, stream, q, k, v, out, lse, dout, workspace) as raw:
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         need = int(lib.mesa_swa_backward_workspace_size(B, Hq, Hkv, T, S, d, _size("sinks", sinks), code))
         workspace = _workspace(workspace, need, dev, index)
@@ -678,7 +683,7 @@ def swa_step(q, k, v, k_cache, v_cache, pos, *, window, sinks=0, scale=None, out
     _arg("pos", pos, (B,), torch.int32, index)
     if out is not None:
         _arg("out", out, q.shape, q.dtype, index)
-    with _On(index, stream) as raw:
+    with _On(index, stream, q, k, v, k_cache, v_cache, pos, out, workspace) as raw:
         out = torch.empty_like(q) if out is None else out
         need = lib.mesa_swa_step_workspace_size(B, Hq, Hkv, d, window, sinks, code)
         if need or workspace is not None:
@@ -701,7 +706,7 @@ def swa_cache_fill(k, v, k_cache, v_cache, *, window, sinks=0, start=0, lens=Non
     _caches(k_cache, v_cache, B, Hkv, _size("sinks", sinks) + _size("window", window), d, k.dtype, index)
     if lens is not None:
         _arg("lens", lens, (B,), torch.int32, index)
-    with _On(index, stream) as raw:
+    with _On(index, stream, k, v, k_cache, v_cache, lens) as raw:
         _check(lib.mesa_swa_cache_fill(_p(k), _p(v), _p(k_cache), _p(v_cache), _p(lens), B, Hkv, S, d,
                                        _size("window", window), _size("sinks", sinks), _size("start", start), _dtype_code(k), raw),
                "mesa_swa_cache_fill")

@@ -651,3 +651,45 @@ def test_first_call_of_a_host_thread(mesa, call):
     assert status == [0]
     for a, b in zip(got, new):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("call", ["lru_forward", "lru_backward", "lru_step", "forward", "backward", "step", "cache_fill"])
+def test_inputs_dropped_while_a_call_is_to_run(mesa, call):
+    """Tensors of one stream, a call on another that is still busy, and their memory given up at once."""
+    g = torch.Generator().manual_seed(81)
+    bf = torch.bfloat16
+
+    def make(*shape, dtype=bf):
+        return torch.randn(shape, generator=g).cuda().to(dtype)
+    x = [make(2, 300, 64) for _ in range(4)]
+    lam, h0 = make(64, dtype=torch.float32) - 4, make(2, 64, dtype=torch.float32)
+    y, saved = mesa.lru_forward(*x[:3], lam, h0=h0, return_saved=True)
+    q, k, v, do = make(2, 4, 300, 64), make(2, 2, 300, 64), make(2, 2, 300, 64), make(2, 4, 300, 64)
+    out, lse = mesa.swa_forward(q, k, v, window=60, return_lse=True)
+    kc, vc, pos = make(2, 2, 60, 64), make(2, 2, 60, 64), torch.tensor([7, 99], dtype=torch.int32, device="cuda")
+    first = [t[:, :, 0].contiguous() for t in (q, k, v)]
+    args, run = {
+        "lru_forward": (x[:3] + [lam, h0], lambda a, s: mesa.lru_forward(*a[:4], h0=a[4], return_state=True, stream=s)),
+        "lru_backward": (x[:3] + [lam, x[3], saved, h0], lambda a, s: mesa.lru_backward(*a[:5], saved=a[5], dh_T=a[6], stream=s)),
+        "lru_step": ([t[:, 0].contiguous() for t in x[:3]] + [lam, h0], lambda a, s: (mesa.lru_step(*a, stream=s),)),
+        "forward": ([q, k, v], lambda a, s: (mesa.swa_forward(*a, window=60, stream=s),)),
+        "backward": ([q, k, v, out, lse, do], lambda a, s: mesa.swa_backward(*a, window=60, stream=s)),
+        "step": (first + [kc, vc, pos], lambda a, s: (mesa.swa_step(*a, window=60, stream=s),)),
+        "cache_fill": ([k, v], lambda a, s: mesa.swa_cache_fill(*a, kd, vd, window=60, stream=s)),
+    }[call]
+    kd, vd = torch.zeros_like(kc), torch.zeros_like(vc)
+    want = run([t.clone() for t in args], None) or (kd.clone(), vd.clone())
+    kd.zero_(), vd.zero_()
+    side = torch.cuda.Stream()
+    copies = [t.clone() for t in args]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)                    # about 50 ms
+    got = run(copies, side) or (kd, vd)
+    shapes = [(t.shape, t.dtype) for t in copies]
+    del copies
+    junk = [torch.full(s, 77 if d == torch.int32 else float("nan"), dtype=d, device="cuda") for s, d in shapes for _ in range(2)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    del junk
