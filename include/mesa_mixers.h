@@ -13,8 +13,10 @@
  * (MESA_ERR_INVALID_ARG) unless stated otherwise. Every result is
  * bit-reproducible from call to call: no floating-point atomics are used.
  * Make one call on a device before capturing calls into a graph there (the
- * first looks up the device's error word). A kernel that gives up a bounded
- * wait records MESA_ERR_DEVICE_TIMEOUT for mesa_get_error().
+ * first looks up the device's error word). Several host threads may call at
+ * once, with workspaces of their own. A kernel that gives up a bounded
+ * wait records MESA_ERR_DEVICE_TIMEOUT for mesa_get_error(); its outputs are
+ * then undefined.
  */
 #ifndef MESA_MIXERS_H
 #define MESA_MIXERS_H
@@ -118,8 +120,11 @@ mesa_status mesa_swa_forward(const void* q, const void* k, const void* v, int B,
  * (dk, dv summed over the query heads that share a head).
  *   dq [B,Hq,T,d];  dk, dv [B,Hkv,S,d]; all in `dtype`, rounded once.
  *   workspace    mesa_swa_backward_workspace_size() bytes, 256-byte aligned.
+ * MESA_BF16 with d = 64 or 128: P and dS round to bf16 before their products.
  * Keys that no query sees get zero gradients (T < S, or T = 0); where every
- * query sees one key alone, dq and dk are exactly zero.
+ * query of the call sees one key alone (S = 1, or a window of 1 without
+ * sinks), dq and dk are exactly zero. In other calls the gradients of a query
+ * that sees one key are zero up to the rounding of dP - delta.
  */
 size_t mesa_swa_backward_workspace_size(int B, int Hq, int Hkv, int T, int S, int d, int sinks, mesa_dtype dtype);
 mesa_status mesa_swa_backward(const void* q, const void* k, const void* v, const void* out, const float* lse,
@@ -144,7 +149,8 @@ mesa_status mesa_swa_backward(const void* q, const void* k, const void* v, const
  *                     (that may be 0: then it may be NULL). Calls sharing a
  *                     workspace must not overlap.
  * All others 16-byte aligned (pos 4). d, sinks, scale as above; window >= 1;
- * sinks + window < 2^31; B * Hq <= 65535.
+ * sinks + window < 2^31; B * Hq <= 65535. MESA_BF16 with d = 64 or 128: the
+ * softmax weights round to bf16 before their product with v, as in the forward.
  */
 size_t mesa_swa_step_workspace_size(int B, int Hq, int Hkv, int d, int window, int sinks, mesa_dtype dtype);
 mesa_status mesa_swa_step(const void* q, const void* k, const void* v, void* k_cache, void* v_cache,

@@ -45,7 +45,8 @@ bool given(std::initializer_list<const void*> ps, size_t align) {
 mesa_status status(cudaError_t e) { return e == cudaSuccess ? MESA_OK : MESA_ERR_CUDA; }
 
 // ---- recurrence ----
-// Grids are one-dimensional: at most 8 CTAs for each 32 channels of a sequence.
+// Grids are one-dimensional: one CTA for each 32 channels or more of a sequence,
+// up to kLruMaxCluster where that leaves SMs idle.
 mesa_status lru_shape(int B, int T, int D, mesa_dtype dtype) {
     if (B < 1 || T < 0 || D < 1 || !dtype_ok(dtype)) return MESA_ERR_INVALID_ARG;
     if (T > (1 << 30) || (long long)B * ((D + 31LL) / 32) > (1LL << 27)) return MESA_ERR_UNSUPPORTED;

@@ -16,6 +16,16 @@
 // (0.79 of the measured copy rate), 102 by clusters. Up to 8 MB of cache the
 // cluster is as fast or faster: its one launch against two.
 //
+// bf16 with d = 64 or 128 rounds the softmax weights to bf16 for their product
+// with v (sums, maxima and parts stay in fp32), as the forward does: a token
+// decoded and the same token in a prompt carry the same roundings. Error
+// against 64 bits for the batch above 0.0021, of which the output's own
+// rounding is 0.0017.
+//
+// The fp32 kernel is plain: a thread reads a K row of its own. 64 sequences of
+// 4100 slots, 4 heads of 128 columns in fp32: 917 us, 1.2 TB/s; bf16, d = 32:
+// 197 us, 0.7 TB/s.
+//
 // The new token's rows are read from the arguments, not from the cache: their
 // slot is written by one CTA while others run, and nobody reads it.
 #include <cooperative_groups.h>

@@ -20,7 +20,8 @@
 // columns wide, in chains the arithmetic warps interrupt; tensor pipe 46 % busy
 // in both kernels. Batch 2, 16 over 4 heads, 8192 tokens, d = 128, window 1024:
 // 638 us in all. Steps of 64 queries let dk, dv run two stages; with 128 their
-// scores and sums leave tensor memory no room for a second.
+// scores and sums leave tensor memory no room for a second at d = 128, and both
+// widths use the same columns.
 #include "swa_tc.cuh"
 
 namespace mesa {

@@ -26,9 +26,13 @@
 // (64-key tiles with two score buffers take the chain apart, but a product of
 // 128 x 64 x 16 takes the tensor pipe as long as one of 128 x 128 x 16.)
 // P is rounded to bf16 for its product with v; the sum l adds it unrounded.
-// Batch 4, 16 heads, 8192 tokens, d = 128, window 1024, 4 sinks: 432 us, 600
-// TFLOP/s of visible pairs, 0.36 of the measured bf16 rate; tensor pipe 36 %,
-// special-function unit 38 % busy.
+// Batch 4, 16 heads, 8192 tokens, d = 128, window 1024, 4 sinks: 425 us by events
+// around the kernel, 467 us a pass through the public call, 600 TFLOP/s of
+// visible pairs, 0.36 of the measured bf16 rate; tensor pipe 36 %,
+// special-function unit 38 % busy. 96 registers a thread, about 140 bytes of them
+// spilled.
+// Both widths use the same columns: at d = 64 the two O take half of theirs, and
+// 128 columns stay unused.
 #include "swa_tc.cuh"
 
 namespace mesa {

@@ -188,3 +188,10 @@ def test_no_kernel_that_no_call_reaches(lib):
             assert f"{kernel}<__nv_bfloat16, {d}>" in names, (kernel, d)
         for d in (64, 128):
             assert f"{kernel}<float, {d}>" in names and f"{kernel}<__nv_bfloat16, {d}>" not in names, (kernel, d)
+
+
+def test_fault_injection_is_in_the_debug_library_alone(lib):
+    from test_sequence_layer_b200 import build
+    assert not hasattr(lib, "mesa_debug_lose_signal")
+    dlib = ctypes.CDLL(build.build(debug=True))
+    assert dlib.mesa_debug_lose_signal(-1) == INVALID
