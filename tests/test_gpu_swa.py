@@ -693,3 +693,21 @@ def test_inputs_dropped_while_a_call_is_to_run(mesa, call):
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     del junk
+
+
+def test_named_stream_while_capturing(mesa):
+    """The capturing stream given by name, an input dropped during the capture."""
+    q, k, v, _ = inputs(1, 4, 2, 200, 260, 128, "bf16", seed=91)
+    want = mesa.swa_forward(q, k, v, window=100, sinks=4)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        doubled = q * 2
+        half = doubled / 2
+        del doubled
+        out = mesa.swa_forward(half, k, v, window=100, sinks=4, stream=torch.cuda.current_stream())
+        del half
+        after = out + 0
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(after, want)
